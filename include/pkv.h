@@ -315,6 +315,85 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
                                  pkv_stream_t stream);
 
 /*
+ * FP8 KV cache with a scale for each block -- the same e4m3 pool, with scales
+ * that follow the tokens instead of calibrated ones: k_scales and v_scales are
+ * device fp32 arrays [num_blocks][num_kv_heads], and the value of a code c of
+ * block b and kv head h is e4m3(c) * scales[b][h].  The pages name FP8 mixed
+ * precision (ai-stack.site "Nano-vLLM 原理", case study) and have no
+ * counterpart of the scales.  A block's scales travel with its codes: copy
+ * both on copy-on-write (pkv_copy_blocks / _dev and pkv_copy_scales / _dev).
+ *
+ * pkv_write_fp8_block: appends tokens and quantises them.  Sequence s gets the
+ *   rows query_start[s] .. query_start[s+1] - 1 of k and v (bf16 [num_tokens]
+ *   [num_kv_heads][head_dim], 16-B aligned) as its last positions:
+ *   context_lens[s] counts them already, and their blocks are in its table
+ *   (as pkv_bm_append_slots leaves both).  For every block that receives rows,
+ *   every kv head, K and V apart:
+ *     a    = the largest finite |x| of the rows it receives
+ *     need = the least power of two >= 2^-126 with a <= 448 * need
+ *     s'   = need if the block holds no older row, else max(scale, need)
+ *     older rows: code = e4m3_rne(e4m3(code) * scale / s')   (unchanged if s' = scale)
+ *     new rows:   code = e4m3_rne_satfinite(x / s')
+ *   and s' becomes the block's scale.  Infinities saturate, NaN stays NaN.
+ *   Rows past query_start[num_seqs] are not read; codes and scales of other
+ *   blocks, and codes past a context, stay as they were.
+ *     query_start     int32 [num_seqs + 1], non-decreasing
+ *     max_new_tokens  host upper bound of the new tokens of a sequence
+ *   Two sequences must not append to the same block (copy it first).  A
+ *   sequence with more new tokens than max_new_tokens or its context, with
+ *   rows outside [0, num_tokens), or longer than its table sets
+ *   PKV_DEVERR_CONTEXT and is left out; a block id outside the pool sets
+ *   PKV_DEVERR_BLOCK and the block is left out.  One kernel, no workspace.
+ *
+ * pkv_copy_scales / pkv_copy_scales_dev: row src -> row dst of both scale
+ *   arrays for every pair, with the rules of pkv_copy_blocks (host pairs) and
+ *   pkv_copy_blocks_dev (device pairs; ids outside the pool set
+ *   PKV_DEVERR_BLOCK and are skipped).
+ *
+ * paged_attn_decode_fp8_block: paged_attn_decode over this pool, at head
+ *   dimensions 64 and 128 and every GQA group <= 16.  Scales are finite and
+ *   above zero for the blocks under a context.  The codes and q (divided by a
+ *   power of two for each head) are multiplied as f16 with fp32 accumulation;
+ *   a softmax weight times its block's V scale enters the weighted sum as f16,
+ *   relative to the largest such product so far, whatever the scales' range
+ *   (so one below 2^-14 of it is rounded to 2^-24 of it).
+ *   The workspace is the same as paged_attn_decode's.
+ */
+pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
+                               int32_t num_tokens, int32_t max_new_tokens, float *k_scales, float *v_scales,
+                               void *k_cache, void *v_cache, pkv_pool pool, pkv_stream_t stream);
+pkv_status pkv_copy_scales(const int32_t *src_dst_pairs, int32_t num_pairs, float *k_scales, float *v_scales,
+                           int32_t num_blocks, int32_t num_kv_heads, pkv_stream_t stream);
+pkv_status pkv_copy_scales_dev(const int32_t *cow_pairs, const int32_t *num_pairs, int32_t max_pairs, float *k_scales,
+                               float *v_scales, int32_t num_blocks, int32_t num_kv_heads, pkv_stream_t stream);
+pkv_status paged_attn_decode_fp8_block(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                                       const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                       int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
+                                       int32_t partition_tokens, void *workspace, size_t workspace_bytes,
+                                       pkv_stream_t stream);
+
+/*
+ * Block-sparse decode -- a decode step over a long context reads only the
+ * blocks that matter to its query: the bounds of every block's keys give an
+ * upper bound of q.k over the block, the best blocks are selected for each
+ * (sequence, kv head), and attention runs over those.  The pages have no
+ * counterpart.
+ *
+ * pkv_key_bounds: bounds[b][h] = the least and the largest element of each
+ *   head-dim column over the keys that block b holds, for the blocks that an
+ *   append touches (arguments as in pkv_write_fp8_block; run it after the
+ *   write).  bounds is bf16 [num_blocks][num_kv_heads][2][head_dim] (least
+ *   first), 16-B aligned; other blocks' bounds stay as they were.  k_scales is
+ *   NULL for a bf16 pool and the block scales of an e4m3 pool (whose values
+ *   are rounded to bf16).  A column with a NaN key has NaN bounds.
+ */
+pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,
+                          int32_t num_seqs, int32_t max_new_tokens, void *bounds, pkv_pool pool, pkv_stream_t stream);
+
+/*
  * Block manager on the device -- the bookkeeping of the pages' block manager
  * (wkbse.com section 3.1, "flexible memory management": blocks allocated only
  * as new tokens need them, the block table updated, blocks returned when a

@@ -29,7 +29,8 @@ EXPORTED = ("pkv_write", "pkv_copy_blocks", "pkv_decode_workspace_bytes", "paged
             "pkv_swap_out", "pkv_swap_in", "pkv_lru_victims", "pkv_bm_state_bytes", "pkv_bm_init", "pkv_bm_alloc",
             "pkv_bm_free", "pkv_bm_share", "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8",
             "paged_attn_decode_fp8", "pkv_prefix_cache_bytes", "pkv_prefix_cache_init", "pkv_prefix_lookup",
-            "pkv_prefix_insert")
+            "pkv_prefix_insert", "pkv_write_fp8_block", "pkv_copy_scales", "pkv_copy_scales_dev",
+            "paged_attn_decode_fp8_block", "pkv_key_bounds")
 STATIC_WS_BYTES = 32 << 20  # PKV_STATIC_WS_BYTES
 
 
@@ -83,13 +84,19 @@ def load_library() -> ctypes.CDLL:
         lib.pkv_prefix_insert.argtypes = [P, I32, P, I32, P, P, I32, I32, P, I32, P]
         lib.paged_attn_decode_fp8.argtypes = [P, P, P, P, P, P, I32, P, I32, I32, F, I32, P, _Pool, I32, I32, P, SZ,
                                               P]
+        lib.pkv_write_fp8_block.argtypes = [P, P, P, I32, P, P, I32, I32, I32, P, P, P, P, _Pool, P]
+        lib.pkv_copy_scales.argtypes = [P, I32, P, P, I32, I32, P]
+        lib.pkv_copy_scales_dev.argtypes = [P, P, I32, P, P, I32, I32, P]
+        lib.paged_attn_decode_fp8_block.argtypes = lib.paged_attn_decode_fp8.argtypes
+        lib.pkv_key_bounds.argtypes = [P, P, P, I32, P, P, I32, I32, P, _Pool, P]
         lib.pkv_status_string.argtypes = [ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
         lib.pkv_version.restype = I32
         for f in ("pkv_write", "pkv_copy_blocks", "paged_attn_decode", "pkv_get_device_error", "pkv_swap_out",
                   "pkv_swap_in", "pkv_lru_victims", "pkv_bm_init", "pkv_bm_alloc", "pkv_bm_free", "pkv_bm_share",
                   "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8", "paged_attn_decode_fp8",
-                  "pkv_prefix_cache_init", "pkv_prefix_lookup", "pkv_prefix_insert"):
+                  "pkv_prefix_cache_init", "pkv_prefix_lookup", "pkv_prefix_insert", "pkv_write_fp8_block",
+                  "pkv_copy_scales", "pkv_copy_scales_dev", "paged_attn_decode_fp8_block", "pkv_key_bounds"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -421,6 +428,155 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         _pool(k_cache), int(max_context_len), int(partition_tokens), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "paged_attn_decode_fp8")
+
+
+def _need_block_scales(k_scales, v_scales, k_cache):
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _need(t, n, torch.float32)
+        if t.shape != k_cache.shape[:2]:
+            raise ValueError(f"{n} must be [num_blocks, num_kv_heads]")
+
+
+def _need_append(block_tables, context_lens, query_start):
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"), (query_start, "query_start")):
+        _need(t, n, torch.int32)
+    B = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.dim() != 1 or query_start.shape != (B + 1,):
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B], query_start [B + 1]")
+
+
+class _one_device:
+    """Every tensor of a call on one GPU, and that GPU current while it runs."""
+
+    def __init__(self, first: torch.Tensor, *others):
+        self.index = index = first.device.index
+        for t in others:
+            if t is not None and t.device.index != index:
+                raise ValueError("all tensors must be on one device")
+        self.previous = torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.index != self.previous:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.index != self.previous:
+            torch.cuda.set_device(self.previous)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream` (None: the current one)."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:  # the allocator may hand the memory on once `stream` is through, not before
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                         else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
+    return ws
+
+
+def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                        query_start: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                        k_cache: torch.Tensor, v_cache: torch.Tensor, max_new_tokens: int, stream=None) -> None:
+    """Appends and quantises: rows query_start[s] .. query_start[s+1] - 1 of k and v become the last positions of
+    sequence s (context_lens counts them), as e4m3 codes with a power-of-two scale for each (block, kv head).  A
+    block that already holds rows keeps its scale or grows it, and its older codes are rounded anew."""
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, torch.bfloat16)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.uint8)
+    _need_append(block_tables, context_lens, query_start)
+    _need_block_scales(k_scales, v_scales, k_cache)
+    T = k.shape[0]
+    if k.shape != (T, k_cache.shape[1], k_cache.shape[3]) or v.shape != k.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim] and the caches alike")
+    with _one_device(k, v, block_tables, context_lens, query_start, k_scales, v_scales, k_cache, v_cache):
+        st = load_library().pkv_write_fp8_block(
+            k.data_ptr(), v.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            query_start.data_ptr(), context_lens.shape[0], T, int(max_new_tokens), k_scales.data_ptr(),
+            v_scales.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _pool(k_cache), _stream(stream))
+    _check(st, "pkv_write_fp8_block")
+
+
+def pkv_copy_scales(src_dst_pairs, k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
+    """Copies row src -> dst of both scale arrays for every (src, dst) host pair: pkv_copy_blocks' companion."""
+    _need_scale_rows(k_scales, v_scales)
+    pairs = np.ascontiguousarray(np.asarray(src_dst_pairs, dtype=np.int32).reshape(-1, 2))
+    with _one_device(k_scales, v_scales):
+        st = load_library().pkv_copy_scales(pairs.ctypes.data_as(ctypes.c_void_p), pairs.shape[0], _ptr(k_scales),
+                                            _ptr(v_scales), k_scales.shape[0], k_scales.shape[1], _stream(stream))
+    _check(st, "pkv_copy_scales")
+
+
+def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                    stream=None) -> None:
+    """Copies row src -> dst of both scale arrays for the first num_pairs[0] rows of the device pair list: the
+    companion of copy_blocks_dev."""
+    _need(cow_pairs, "cow_pairs", torch.int32)
+    _need(num_pairs, "num_pairs", torch.int32)
+    _need_scale_rows(k_scales, v_scales)
+    with _one_device(k_scales, v_scales, cow_pairs, num_pairs):
+        st = load_library().pkv_copy_scales_dev(_ptr(cow_pairs), _ptr(num_pairs), cow_pairs.shape[0], _ptr(k_scales),
+                                                _ptr(v_scales), k_scales.shape[0], k_scales.shape[1], _stream(stream))
+    _check(st, "pkv_copy_scales_dev")
+
+
+def _need_scale_rows(k_scales, v_scales):
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _need(t, n, torch.float32)
+    if k_scales.dim() != 2 or v_scales.shape != k_scales.shape:
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+
+
+def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                                v_scales: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                scale: float, num_kv_heads: int, out: torch.Tensor, max_context_len: int,
+                                partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """paged_attn_decode over an FP8 (e4m3) pool with a K and a V scale for each (block, kv head)."""
+    for t, n in ((q, "q"), (out, "out")):
+        _need(t, n, torch.bfloat16)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.uint8)
+    _need(block_tables, "block_tables", torch.int32)
+    _need(context_lens, "context_lens", torch.int32)
+    _need_block_scales(k_scales, v_scales, k_cache)
+    B, Hq, D = q.shape
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or D != k_cache.shape[3]:
+        raise ValueError("out must match q, v_cache must match k_cache, and their head dimensions agree")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    if workspace is None:
+        workspace = _scratch(decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens),
+                             q.device, stream)
+    with _one_device(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, out, workspace):
+        st = load_library().paged_attn_decode_fp8_block(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale),
+            int(num_kv_heads), out.data_ptr(), _pool(k_cache), int(max_context_len), int(partition_tokens),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "paged_attn_decode_fp8_block")
+
+
+def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                   query_start: torch.Tensor, bounds: torch.Tensor, max_new_tokens: int,
+                   k_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """bounds[b][h][0 / 1] = the least / largest key element of each column over the rows that block b holds, for
+    the blocks that an append (query_start as in pkv_write_fp8_block) touches; bounds is bf16 [num_blocks,
+    num_kv_heads, 2, head_dim].  k_scales: the block scales of an e4m3 pool, None for a bf16 one."""
+    _need_cache(k_cache, "k_cache")
+    _need_append(block_tables, context_lens, query_start)
+    _need(bounds, "bounds", torch.bfloat16)
+    if bounds.shape != (k_cache.shape[0], k_cache.shape[1], 2, k_cache.shape[3]):
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    if (k_scales is not None) != (k_cache.dtype == torch.uint8):
+        raise ValueError("k_scales belong to an e4m3 pool, and only there")
+    if k_scales is not None:
+        _need_block_scales(k_scales, k_scales, k_cache)
+    with _one_device(k_cache, block_tables, context_lens, query_start, bounds, k_scales):
+        st = load_library().pkv_key_bounds(
+            k_cache.data_ptr(), None if k_scales is None else k_scales.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), context_lens.shape[0],
+            int(max_new_tokens), bounds.data_ptr(), _pool(k_cache), _stream(stream))
+    _check(st, "pkv_key_bounds")
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -14,6 +14,7 @@
 #include <mutex>
 #include <vector>
 
+#include "block_cache.cuh"
 #include "block_manager.cuh"
 #include "decode.cuh"
 #include "pkv.h"
@@ -105,18 +106,19 @@ bool encode_pool_map(CUtensorMap *map, const void *base, const pkv_pool &pool) {
     return r == CUDA_SUCCESS;
 }
 
-// An FP8 pool (e4m3 codes) as 2-D [rows][D] bytes; a box is 16 rows x 128
-// bytes, the whole row at head dim 128.
+// An FP8 pool (e4m3 codes) as 2-D [rows][D] bytes; a box is 16 rows of the
+// whole row: 128 bytes with the 128-byte swizzle, or 64 with the 64-byte one.
 bool encode_pool_map_u8(CUtensorMap *map, const void *base, const pkv_pool &pool) {
     auto fn = encode_fn();
-    if (!fn || pool.head_dim != 128) return false;
+    if (!fn) return false;
     const cuuint64_t rows = (cuuint64_t)pool.num_blocks * pool.num_kv_heads * pool.block_size;
     cuuint64_t dims[2] = {(cuuint64_t)pool.head_dim, rows};
     cuuint64_t strides[1] = {(cuuint64_t)pool.head_dim};
-    cuuint32_t box[2] = {128, (cuuint32_t)pkv::kStageTok};
+    cuuint32_t box[2] = {(cuuint32_t)pool.head_dim, (cuuint32_t)pkv::kStageTok};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          pool.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -171,12 +173,12 @@ bool workspace_layout(int32_t B, int32_t Hq, int32_t D, int32_t max_ctx, int32_t
 
 // ---------------------------------------------------- decode dispatch ----
 
-template <int D, int PATH, int GS, int GPAD, bool KV8 = false>
+template <int D, int PATH, int GS, int GPAD, bool KV8 = false, bool KVB = false>
 pkv_status launch_decode(const pkv::DecodeParams &prm, const CUtensorMap &mk, const CUtensorMap &mv,
                          cudaStream_t stream, int dev) {
     constexpr int NS = PATH == 0 ? kStagesSimt : kStagesMma;
-    using L = pkv::DecodeSmem<D, (PATH == 0 ? GS : GPAD), NS, KV8>;
-    auto kernel = pkv::paged_decode_kernel<D, PATH, GS, GPAD, NS, KV8>;
+    using L = pkv::DecodeSmem<D, (PATH == 0 ? GS : GPAD), NS, KV8, KVB>;
+    auto kernel = pkv::paged_decode_kernel<D, PATH, GS, GPAD, NS, KV8, KVB>;
     // the shared-memory attribute is set before the occupancy query, so a
     // cached occupancy also means the attribute is set on this device
     static DeviceCache occ_cache{};
@@ -224,6 +226,18 @@ pkv_status dispatch_group(int g, const pkv::DecodeParams &prm, const CUtensorMap
     if (g <= 4) return launch_decode<D, 1, 1, 4>(prm, mk, mv, stream, dev);
     if (g <= 8) return launch_decode<D, 1, 1, 8>(prm, mk, mv, stream, dev);
     return launch_decode<D, 1, 1, 16>(prm, mk, mv, stream, dev);
+}
+
+// An FP8 pool.  g = 2 runs on the tensor cores too: over e4m3 codes the
+// CUDA-core body is issue-bound (a conversion and four unpacked FMAs per code
+// pair).
+template <int D, bool KVB>
+pkv_status dispatch_group_fp8(int g, const pkv::DecodeParams &prm, const CUtensorMap &mk, const CUtensorMap &mv,
+                              cudaStream_t stream, int dev) {
+    if (g == 1) return launch_decode<D, 0, 1, 1, true, KVB>(prm, mk, mv, stream, dev);
+    if (g <= 4) return launch_decode<D, 1, 1, 4, true, KVB>(prm, mk, mv, stream, dev);
+    if (g <= 8) return launch_decode<D, 1, 1, 8, true, KVB>(prm, mk, mv, stream, dev);
+    return launch_decode<D, 1, 1, 16, true, KVB>(prm, mk, mv, stream, dev);
 }
 
 // -------------------------------------------------------- prefill ----
@@ -381,10 +395,65 @@ bool prefix_cache(void *cache, int32_t cap, pkv::PrefixCache *c) {
     return true;
 }
 
-// Decode over a bf16 pool (scales null) or an FP8 (e4m3) pool with per-kv-head
-// dequantisation scales (head dim 128, GQA group <= 2: the CUDA-core path).
+// What pkv_write_fp8_block and pkv_key_bounds share: the touched blocks of an
+// append.  PKV_OK with T = 0 in *t means that there is nothing to do.
+pkv_status touch_params(const pkv_pool &pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                        const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
+                        int32_t max_new_tokens, pkv::TouchParams *t) {
+    const pkv_status ps = check_pool(pool);
+    if (ps != PKV_OK) return ps;
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_new_tokens < 0) return PKV_EINVAL;
+    t->B = num_seqs;
+    t->max_new = max_new_tokens;
+    if (num_seqs == 0 || max_new_tokens == 0) return PKV_OK;
+    if (!block_tables || !context_lens || !query_start) return PKV_EINVAL;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4)) return PKV_EINVAL;
+    t->tables = block_tables;
+    t->ctx = context_lens;
+    t->start = query_start;
+    t->MBS = max_blocks_per_seq;
+    t->bs = pool.block_size;
+    t->NB = pool.num_blocks;
+    t->H = pool.num_kv_heads;
+    const long long J = ((long long)max_new_tokens + pool.block_size - 2) / pool.block_size + 1;
+    t->J = (int)std::min<long long>(J, max_blocks_per_seq);
+    return PKV_OK;
+}
+
+// Warps of a team, and the launch of `units` teams.
+int touch_warps(const pkv_pool &pool) { return std::min(pool.block_size / pkv::kTouchRows, pkv::kTouchMaxWarps); }
+
+bool touch_grid(long long units, int W, unsigned *grid, unsigned *threads) {
+    const long long ctas = W > 1 ? units : (units + pkv::kTouchTeams - 1) / pkv::kTouchTeams;
+    if (ctas > 0x7fffffffll) return false;
+    *grid = (unsigned)ctas;
+    *threads = 32u * (W > 1 ? W : pkv::kTouchTeams);
+    return true;
+}
+
+// Validates host pairs of a block copy: ids inside the pool, every destination
+// once and no pair's source.
+pkv_status check_pairs(const int32_t *src_dst_pairs, int32_t num_pairs, int32_t num_blocks) {
+    std::vector<int32_t> src(num_pairs), dst(num_pairs);
+    for (int i = 0; i < num_pairs; ++i) {
+        src[i] = src_dst_pairs[2 * i];
+        dst[i] = src_dst_pairs[2 * i + 1];
+        if (src[i] < 0 || src[i] >= num_blocks || dst[i] < 0 || dst[i] >= num_blocks) return PKV_ERANGE;
+    }
+    std::sort(src.begin(), src.end());
+    std::sort(dst.begin(), dst.end());
+    for (int i = 1; i < num_pairs; ++i)
+        if (dst[i] == dst[i - 1]) return PKV_EALIAS;
+    for (int i = 0; i < num_pairs; ++i)
+        if (std::binary_search(src.begin(), src.end(), dst[i])) return PKV_EALIAS;
+    return PKV_OK;
+}
+
+// Decode over a bf16 pool (scales null) or an FP8 (e4m3) pool: with per-kv-head
+// dequantisation scales (head dim 128), or, `block_scales`, with one for each
+// block and kv head.
 pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
-                       const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                       const float *v_scale, bool block_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
                        int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
                        int32_t partition_tokens, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
@@ -397,7 +466,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     if (num_kv_heads != pool.num_kv_heads || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
     const int g = num_q_heads / num_kv_heads;
     if (g > 16) return PKV_EUNSUPPORTED;
-    if (kv8 && pool.head_dim != 128) return PKV_EUNSUPPORTED;
+    if (kv8 && !block_scales && pool.head_dim != 128) return PKV_EUNSUPPORTED;
     if (partition_tokens < 0 || partition_tokens % 16 != 0 || partition_tokens > 65536) return PKV_EINVAL;
     if (num_seqs == 0) return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace) return PKV_EINVAL;
@@ -433,8 +502,13 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     prm.maxP = (int)std::max<long long>(1, ((long long)max_context_len + PT - 1) / PT);
     prm.pool_rows = pool.num_blocks * pool.num_kv_heads * pool.block_size;
     prm.scale_log2 = scale * 1.4426950408889634f;
-    prm.k_scale = k_scale;
-    prm.v_scale = v_scale;
+    if (block_scales) {
+        prm.kb_scales = k_scale;
+        prm.vb_scales = v_scale;
+    } else {
+        prm.k_scale = k_scale;
+        prm.v_scale = v_scale;
+    }
 
     CUtensorMap mk, mv;
     if (kv8) {
@@ -448,14 +522,10 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     pkv_status r = launch_status();
     if (r != PKV_OK) return r;
     const int dev = current_device();
-    if (kv8) {
-        // g = 2 runs on the tensor cores too: over e4m3 codes the CUDA-core body
-        // is issue-bound (a conversion and four unpacked FMAs per code pair)
-        if (g == 1) return launch_decode<128, 0, 1, 1, true>(prm, mk, mv, st, dev);
-        if (g <= 4) return launch_decode<128, 1, 1, 4, true>(prm, mk, mv, st, dev);
-        if (g <= 8) return launch_decode<128, 1, 1, 8, true>(prm, mk, mv, st, dev);
-        return launch_decode<128, 1, 1, 16, true>(prm, mk, mv, st, dev);
-    }
+    if (block_scales)
+        return D == 128 ? dispatch_group_fp8<128, true>(g, prm, mk, mv, st, dev)
+                        : dispatch_group_fp8<64, true>(g, prm, mk, mv, st, dev);
+    if (kv8) return dispatch_group_fp8<128, false>(g, prm, mk, mv, st, dev);
     return D == 128 ? dispatch_group<128>(g, prm, mk, mv, st, dev) : dispatch_group<64>(g, prm, mk, mv, st, dev);
 }
 
@@ -514,19 +584,8 @@ pkv_status pkv_copy_blocks(const int32_t *src_dst_pairs, int32_t num_pairs, void
     if (num_pairs == 0) return PKV_OK;
     if (!src_dst_pairs || !k_cache || !v_cache) return PKV_EINVAL;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PKV_EINVAL;
-    std::vector<int32_t> src(num_pairs), dst(num_pairs);
-    for (int i = 0; i < num_pairs; ++i) {
-        src[i] = src_dst_pairs[2 * i];
-        dst[i] = src_dst_pairs[2 * i + 1];
-        if (src[i] < 0 || src[i] >= pool.num_blocks || dst[i] < 0 || dst[i] >= pool.num_blocks) return PKV_ERANGE;
-    }
-    std::sort(src.begin(), src.end());
-    std::vector<int32_t> dsorted(dst);
-    std::sort(dsorted.begin(), dsorted.end());
-    for (int i = 1; i < num_pairs; ++i)
-        if (dsorted[i] == dsorted[i - 1]) return PKV_EALIAS;
-    for (int i = 0; i < num_pairs; ++i)
-        if (std::binary_search(src.begin(), src.end(), dsorted[i])) return PKV_EALIAS;
+    const pkv_status cs = check_pairs(src_dst_pairs, num_pairs, pool.num_blocks);
+    if (cs != PKV_OK) return cs;
 
     const int64_t vec = (int64_t)pool.num_kv_heads * pool.block_size * pool.head_dim * elem_bytes(pool) / 16;
     for (int base = 0; base < num_pairs; base += pkv::kMaxPairsPerLaunch) {
@@ -586,7 +645,7 @@ pkv_status paged_attn_decode(const void *q, const void *k_cache, const void *v_c
                              int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out, pkv_pool pool,
                              int32_t max_context_len, int32_t partition_tokens, void *workspace,
                              size_t workspace_bytes, pkv_stream_t stream) {
-    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, block_tables, max_blocks_per_seq, context_lens,
+    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_tables, max_blocks_per_seq, context_lens,
                        num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
                        workspace, workspace_bytes, stream);
 }
@@ -598,7 +657,7 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
                                  int32_t partition_tokens, void *workspace, size_t workspace_bytes,
                                  pkv_stream_t stream) {
     if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return PKV_EINVAL;
-    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq, context_lens,
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, false, block_tables, max_blocks_per_seq, context_lens,
                        num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
                        workspace, workspace_bytes, stream);
 }
@@ -631,6 +690,116 @@ pkv_status pkv_write_fp8(const void *k, const void *v, const int64_t *slot_mappi
     const int dev = current_device();
     const long long blocks = std::min<long long>((p.total + 255) / 256, (long long)sm_count(dev) * 16);
     pkv::kv_write_fp8_kernel<<<(unsigned)std::max<long long>(blocks, 1), 256, 0, (cudaStream_t)stream>>>(p);
+    return launch_status();
+}
+
+pkv_status paged_attn_decode_fp8_block(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                                       const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                       int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
+                                       int32_t partition_tokens, void *workspace, size_t workspace_bytes,
+                                       pkv_stream_t stream) {
+    if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4)) return PKV_EINVAL;
+    return decode_impl(q, k_cache, v_cache, k_scales, v_scales, true, block_tables, max_blocks_per_seq, context_lens,
+                       num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
+                       workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
+                               int32_t num_tokens, int32_t max_new_tokens, float *k_scales, float *v_scales,
+                               void *k_cache, void *v_cache, pkv_pool pool, pkv_stream_t stream) {
+    pkv::WriteBlockParams p;
+    const pkv_status ps = touch_params(pool, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                                       max_new_tokens, &p.t);
+    if (ps != PKV_OK) return ps;
+    if (pool.kv_dtype != PKV_KV_E4M3 || num_tokens < 0) return PKV_EINVAL;
+    if (num_seqs == 0 || num_tokens == 0 || max_new_tokens == 0) return PKV_OK;
+    if (!k || !v || !k_cache || !v_cache || !k_scales || !v_scales) return PKV_EINVAL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return PKV_EINVAL;
+    p.t.T = num_tokens;
+    p.k = static_cast<const uint4 *>(k);
+    p.v = static_cast<const uint4 *>(v);
+    p.k_cache = static_cast<uint2 *>(k_cache);
+    p.v_cache = static_cast<uint2 *>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.units = (long long)num_seqs * p.t.J * p.t.H * 2;
+    p.W = touch_warps(pool);
+    unsigned grid, threads;
+    if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (pool.head_dim == 128) pkv::write_fp8_block_kernel<128><<<grid, threads, 0, st>>>(p);
+    else pkv::write_fp8_block_kernel<64><<<grid, threads, 0, st>>>(p);
+    return launch_status();
+}
+
+pkv_status pkv_copy_scales(const int32_t *src_dst_pairs, int32_t num_pairs, float *k_scales, float *v_scales,
+                           int32_t num_blocks, int32_t num_kv_heads, pkv_stream_t stream) {
+    if (num_pairs < 0 || num_blocks <= 0 || num_kv_heads <= 0) return PKV_EINVAL;
+    if (num_pairs == 0) return PKV_OK;
+    if (!src_dst_pairs || !k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4)) return PKV_EINVAL;
+    if (num_kv_heads > (1 << 20)) return PKV_EUNSUPPORTED;
+    const pkv_status cs = check_pairs(src_dst_pairs, num_pairs, num_blocks);
+    if (cs != PKV_OK) return cs;
+    pkv::CopyScalesParams p;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.H = num_kv_heads;
+    for (int base = 0; base < num_pairs; base += pkv::kScalePairs) {
+        p.n = std::min(pkv::kScalePairs, num_pairs - base);
+        for (int i = 0; i < p.n; ++i)
+            p.pairs[i] = make_int2(src_dst_pairs[2 * (base + i)], src_dst_pairs[2 * (base + i) + 1]);
+        pkv::copy_scales_kernel<<<(unsigned)((p.n * p.H + 255) / 256), 256, 0, (cudaStream_t)stream>>>(p);
+        const pkv_status st = launch_status();
+        if (st != PKV_OK) return st;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_copy_scales_dev(const int32_t *cow_pairs, const int32_t *num_pairs, int32_t max_pairs, float *k_scales,
+                               float *v_scales, int32_t num_blocks, int32_t num_kv_heads, pkv_stream_t stream) {
+    if (max_pairs < 0 || num_blocks <= 0 || num_kv_heads <= 0) return PKV_EINVAL;
+    if (max_pairs == 0) return PKV_OK;
+    if (!cow_pairs || !num_pairs || !k_scales || !v_scales) return PKV_EINVAL;
+    if (!aligned(cow_pairs, 4) || !aligned(num_pairs, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return PKV_EINVAL;
+    const long long n = (long long)max_pairs * num_kv_heads;
+    const unsigned grid = (unsigned)std::min<long long>((n + 255) / 256, 8ll * sm_count(current_device()));
+    pkv::copy_scales_dev_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(k_scales, v_scales, cow_pairs, num_pairs,
+                                                                       max_pairs, num_blocks, num_kv_heads);
+    return launch_status();
+}
+
+pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,
+                          int32_t num_seqs, int32_t max_new_tokens, void *bounds, pkv_pool pool, pkv_stream_t stream) {
+    pkv::KeyBoundsParams p;
+    const pkv_status ps = touch_params(pool, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                                       max_new_tokens, &p.t);
+    if (ps != PKV_OK) return ps;
+    if (num_seqs == 0 || max_new_tokens == 0) return PKV_OK;
+    const bool kv8 = pool.kv_dtype == PKV_KV_E4M3;
+    if (!k_cache || !bounds || !aligned(k_cache, 16) || !aligned(bounds, 16)) return PKV_EINVAL;
+    if (kv8 != (k_scales != nullptr) || !aligned(k_scales, 4)) return PKV_EINVAL;
+    p.t.T = 0x7fffffff;  // only the counts of the new tokens are used
+    p.k_cache = k_cache;
+    p.k_scales = k_scales;
+    p.bounds = static_cast<uint4 *>(bounds);
+    p.units = (long long)num_seqs * p.t.J * p.t.H;
+    p.W = touch_warps(pool);
+    unsigned grid, threads;
+    if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (pool.head_dim == 128) {
+        if (kv8) pkv::key_bounds_kernel<128, true><<<grid, threads, 0, st>>>(p);
+        else pkv::key_bounds_kernel<128, false><<<grid, threads, 0, st>>>(p);
+    } else {
+        if (kv8) pkv::key_bounds_kernel<64, true><<<grid, threads, 0, st>>>(p);
+        else pkv::key_bounds_kernel<64, false><<<grid, threads, 0, st>>>(p);
+    }
     return launch_status();
 }
 
