@@ -394,6 +394,49 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
                           int32_t num_seqs, int32_t max_new_tokens, void *bounds, pkv_pool pool, pkv_stream_t stream);
 
 /*
+ * pkv_select_blocks: for every sequence s and kv head h, the num_selected
+ *   logical blocks that decode attention keeps.  With the head's query heads
+ *   q_j (hq / (num_q_heads / num_kv_heads) = h) and the bounds lo, hi of block b,
+ *     score(b) = max_j sum_d max(q_jd * lo_d, q_jd * hi_d)
+ *   is at least every q_j.k of the block's keys.  Kept are the first block, the
+ *   block that holds the context's last token, and the best others by (score,
+ *   lower index), num_selected in all, or every block of a shorter context.
+ *   The ranking is that of scores in fp64; a NaN score counts as +infinity.
+ *     q         bf16 [num_seqs][num_q_heads][head_dim], 16-B aligned
+ *     bounds    as pkv_key_bounds leaves it (pool gives its sizes; either kv_dtype)
+ *     selected  int32 [num_seqs][num_kv_heads][num_selected], num_selected >= 2:
+ *               ascending logical blocks, then -1
+ *     max_context_len  host upper bound of context_lens; above 8 * 13000 blocks
+ *               (or the table's length, if less) gives PKV_EUNSUPPORTED
+ *   A context length < 0 or above the table / max_context_len sets
+ *   PKV_DEVERR_CONTEXT and is clamped; a block id outside the pool sets
+ *   PKV_DEVERR_BLOCK and scores -infinity.  One kernel, no workspace.
+ *
+ * paged_attn_decode_sparse: paged_attn_decode over the rows of the selected
+ *   blocks that lie under the context: i runs over the positions of blocks
+ *   selected[s][h][..], and the softmax is taken over those.
+ *     selected  int32 [num_seqs][num_kv_heads][num_selected], num_selected >= 1,
+ *               logical blocks in any order; a negative entry is none, an entry
+ *               behind the context's last block sets PKV_DEVERR_BLOCK and is
+ *               none, and a block listed twice counts twice.  No valid entry
+ *               (or an empty context) gives a zero output row.
+ *     k_scales, v_scales  NULL for a bf16 pool; the block scales of an e4m3 pool
+ *   Both pools at head dimensions 64 and 128 and every GQA group <= 16, with
+ *   the arithmetic of paged_attn_decode and paged_attn_decode_fp8_block.
+ *   num_selected up to about 10000 blocks (more: PKV_EUNSUPPORTED).  One
+ *   kernel, no workspace.
+ */
+pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t num_kv_heads, pkv_pool pool, int32_t *selected,
+                             int32_t num_selected, int32_t max_context_len, pkv_stream_t stream);
+pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                                    const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *context_lens, const int32_t *selected, int32_t num_selected,
+                                    int32_t num_seqs, int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out,
+                                    pkv_pool pool, pkv_stream_t stream);
+
+/*
  * Block manager on the device -- the bookkeeping of the pages' block manager
  * (wkbse.com section 3.1, "flexible memory management": blocks allocated only
  * as new tokens need them, the block table updated, blocks returned when a

@@ -30,7 +30,7 @@ EXPORTED = ("pkv_write", "pkv_copy_blocks", "pkv_decode_workspace_bytes", "paged
             "pkv_bm_free", "pkv_bm_share", "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8",
             "paged_attn_decode_fp8", "pkv_prefix_cache_bytes", "pkv_prefix_cache_init", "pkv_prefix_lookup",
             "pkv_prefix_insert", "pkv_write_fp8_block", "pkv_copy_scales", "pkv_copy_scales_dev",
-            "paged_attn_decode_fp8_block", "pkv_key_bounds")
+            "paged_attn_decode_fp8_block", "pkv_key_bounds", "pkv_select_blocks", "paged_attn_decode_sparse")
 STATIC_WS_BYTES = 32 << 20  # PKV_STATIC_WS_BYTES
 
 
@@ -89,6 +89,8 @@ def load_library() -> ctypes.CDLL:
         lib.pkv_copy_scales_dev.argtypes = [P, P, I32, P, P, I32, I32, P]
         lib.paged_attn_decode_fp8_block.argtypes = lib.paged_attn_decode_fp8.argtypes
         lib.pkv_key_bounds.argtypes = [P, P, P, I32, P, P, I32, I32, P, _Pool, P]
+        lib.pkv_select_blocks.argtypes = [P, P, P, I32, P, I32, I32, I32, _Pool, P, I32, I32, P]
+        lib.paged_attn_decode_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, I32, I32, F, I32, P, _Pool, P]
         lib.pkv_status_string.argtypes = [ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
         lib.pkv_version.restype = I32
@@ -96,7 +98,8 @@ def load_library() -> ctypes.CDLL:
                   "pkv_swap_in", "pkv_lru_victims", "pkv_bm_init", "pkv_bm_alloc", "pkv_bm_free", "pkv_bm_share",
                   "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8", "paged_attn_decode_fp8",
                   "pkv_prefix_cache_init", "pkv_prefix_lookup", "pkv_prefix_insert", "pkv_write_fp8_block",
-                  "pkv_copy_scales", "pkv_copy_scales_dev", "paged_attn_decode_fp8_block", "pkv_key_bounds"):
+                  "pkv_copy_scales", "pkv_copy_scales_dev", "paged_attn_decode_fp8_block", "pkv_key_bounds",
+                  "pkv_select_blocks", "paged_attn_decode_sparse"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -577,6 +580,65 @@ def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_le
             block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), context_lens.shape[0],
             int(max_new_tokens), bounds.data_ptr(), _pool(k_cache), _stream(stream))
     _check(st, "pkv_key_bounds")
+
+
+def _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads):
+    _need(q, "q", torch.bfloat16)
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"), (selected, "selected")):
+        _need(t, n, torch.int32)
+    B = q.shape[0]
+    if q.dim() != 3 or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("q must be [B, num_q_heads, head_dim], block_tables [B, max_blocks_per_seq], context_lens [B]")
+    if selected.dim() != 3 or selected.shape[:2] != (B, num_kv_heads):
+        raise ValueError("selected must be [B, num_kv_heads, num_selected]")
+
+
+def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      num_kv_heads: int, block_size: int, selected: torch.Tensor, max_context_len: int,
+                      stream=None) -> None:
+    """selected[s][h] (int32 [B, num_kv_heads, K], K >= 2) := the logical blocks that decode attention of sequence s
+    and kv head h keeps: the first, the last, and the best others by the upper bound of q.k that bounds
+    (pkv_key_bounds) give, ascending; a context of at most K blocks keeps all, and -1 fills the row."""
+    _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads)
+    _need(bounds, "bounds", torch.bfloat16)
+    if bounds.dim() != 4 or bounds.shape[1:] != (num_kv_heads, 2, q.shape[2]):
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    pool = _Pool(bounds.shape[0], bounds.shape[1], int(block_size), bounds.shape[3], KV_BF16)
+    with _one_device(q, bounds, block_tables, context_lens, selected):
+        st = load_library().pkv_select_blocks(
+            q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            q.shape[0], q.shape[1], int(num_kv_heads), pool, selected.data_ptr(), selected.shape[2],
+            int(max_context_len), _stream(stream))
+    _check(st, "pkv_select_blocks")
+
+
+def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                             block_tables: torch.Tensor, context_lens: torch.Tensor, selected: torch.Tensor,
+                             scale: float, num_kv_heads: int, out: torch.Tensor,
+                             k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                             stream=None) -> None:
+    """paged_attn_decode over the rows of the logical blocks selected[s][h] (negative entries: none) that lie under
+    the context.  A bf16 pool, or an e4m3 pool with its block scales."""
+    _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads)
+    _need(out, "out", torch.bfloat16)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need_cache(t, n)
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("out must match q, v_cache must match k_cache, and their head dimensions agree")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must have the same element type")
+    fp8 = k_cache.dtype == torch.uint8
+    if (k_scales is not None) != fp8 or (v_scales is not None) != fp8:
+        raise ValueError("k_scales and v_scales belong to an e4m3 pool, and only there")
+    if fp8:
+        _need_block_scales(k_scales, v_scales, k_cache)
+    with _one_device(q, k_cache, v_cache, block_tables, context_lens, selected, out, k_scales, v_scales):
+        st = load_library().paged_attn_decode_sparse(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
+            v_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), selected.data_ptr(), selected.shape[2], q.shape[0], q.shape[1], float(scale),
+            int(num_kv_heads), out.data_ptr(), _pool(k_cache), _stream(stream))
+    _check(st, "paged_attn_decode_sparse")
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -436,16 +436,16 @@ struct SimtState {
             kscale *= up;
 #pragma unroll
             for (int e = 0; e < EPL; e += 2) q16[e / 2] = f16x2_from_f32(x[e] * down, x[e + 1] * down);
-            return;
-        }
+        } else {
 #pragma unroll
-        for (int e = 0; e < EPL; e += 2) {
-            const uint32_t pr = *reinterpret_cast<const uint32_t *>(qs + lane * EPL + e);
-            if constexpr (KV8) {
-                q16[e / 2] = f16x2_from_f32(bf16lo_to_f32(pr), bf16hi_to_f32(pr));
-            } else {
-                q[e] = bf16lo_to_f32(pr) * scale_log2;
-                q[e + 1] = bf16hi_to_f32(pr) * scale_log2;
+            for (int e = 0; e < EPL; e += 2) {
+                const uint32_t pr = *reinterpret_cast<const uint32_t *>(qs + lane * EPL + e);
+                if constexpr (KV8) {
+                    q16[e / 2] = f16x2_from_f32(bf16lo_to_f32(pr), bf16hi_to_f32(pr));
+                } else {
+                    q[e] = bf16lo_to_f32(pr) * scale_log2;
+                    q[e + 1] = bf16hi_to_f32(pr) * scale_log2;
+                }
             }
         }
     }

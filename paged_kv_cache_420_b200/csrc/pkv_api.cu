@@ -16,7 +16,9 @@
 
 #include "block_cache.cuh"
 #include "block_manager.cuh"
+#include "block_select.cuh"
 #include "decode.cuh"
+#include "decode_sparse.cuh"
 #include "pkv.h"
 #include "prefill.cuh"
 #include "prefill_tc.cuh"
@@ -238,6 +240,107 @@ pkv_status dispatch_group_fp8(int g, const pkv::DecodeParams &prm, const CUtenso
     if (g <= 4) return launch_decode<D, 1, 1, 4, true, KVB>(prm, mk, mv, stream, dev);
     if (g <= 8) return launch_decode<D, 1, 1, 8, true, KVB>(prm, mk, mv, stream, dev);
     return launch_decode<D, 1, 1, 16, true, KVB>(prm, mk, mv, stream, dev);
+}
+
+// --------------------------------------------- block-sparse decode ----
+
+// A launch of clusters of `splits` CTAs, allowed to start its prologue while
+// the stream's previous kernel ends.
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(long long ctas, int threads, size_t smem, int splits, cudaStream_t stream) {
+        std::memset(&cfg, 0, sizeof cfg);
+        std::memset(attr, 0, sizeof attr);
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)splits;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+constexpr size_t kMaxDynamicSmem = 227 * 1024;
+
+// Raises a kernel's dynamic shared memory limit to the device's, once per device.
+template <typename Kernel>
+bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
+    if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire) != 0) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamicSmem) != cudaSuccess)
+        return false;
+    if (dev >= 0 && dev < kMaxDevices) done[dev].store(1, std::memory_order_release);
+    return true;
+}
+
+constexpr int kSparseMaxSplits = 8;
+
+// CTAs of a (sequence, kv head): as many as fill the GPU's SMs four times,
+// while each still has 8 stages (two of every consumer warp).
+int sparse_splits(long long units, long long stages, int sms) {
+    int splits = 1;
+    while (splits < kSparseMaxSplits && units * splits < 4ll * sms && stages / (2 * splits) >= 8) splits *= 2;
+    return splits;
+}
+
+template <int D, int PATH, int GPAD, bool KV8>
+pkv_status launch_sparse(pkv::SparseParams prm, long long units, const CUtensorMap &mk, const CUtensorMap &mv,
+                         cudaStream_t stream) {
+    constexpr int NS = PATH == 0 ? kStagesSimt : kStagesMma;
+    using L = pkv::SparseSmem<D, GPAD, NS, KV8>;
+    auto kernel = pkv::sparse_decode_kernel<D, PATH, GPAD, NS, KV8>;
+    const int dev = current_device();
+    static DeviceCache done{};
+    if (!allow_smem(kernel, done, dev)) return PKV_ECUDA;
+    const int spe = prm.bs / pkv::kStageTok;
+    const long long stages = (long long)prm.K * spe;
+    prm.splits = sparse_splits(units, stages, sm_count(dev));
+    const long long per = (stages + prm.splits - 1) / prm.splits;
+    prm.share = (int)std::min<long long>(prm.K, (per + spe - 1) / spe + 1);
+    const size_t smem = L::bytes(prm.share);
+    if (smem > kMaxDynamicSmem || units * prm.splits > 0x7fffffffll) return PKV_EUNSUPPORTED;
+    ClusterLaunch cl(units * prm.splits, pkv::kDecodeThreads, smem, prm.splits, stream);
+    if (cudaLaunchKernelEx(&cl.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
+    return launch_status();
+}
+
+template <int D, bool KV8>
+pkv_status dispatch_sparse(const pkv::SparseParams &prm, long long units, const CUtensorMap &mk, const CUtensorMap &mv,
+                           cudaStream_t stream) {
+    if (prm.g == 1) return launch_sparse<D, 0, 1, KV8>(prm, units, mk, mv, stream);
+    if (prm.g <= 4) return launch_sparse<D, 1, 4, KV8>(prm, units, mk, mv, stream);
+    if (prm.g <= 8) return launch_sparse<D, 1, 8, KV8>(prm, units, mk, mv, stream);
+    return launch_sparse<D, 1, 16, KV8>(prm, units, mk, mv, stream);
+}
+
+constexpr int kSelectMinBlocks = 64;  // blocks of a CTA, below which a unit is not split further
+
+size_t select_smem(long long cap) { return (sizeof(pkv::SelectSmem) + 15) / 16 * 16 + (size_t)((cap + 3) / 4 * 4) * 16; }
+
+template <int D, bool TALL>
+pkv_status launch_select(pkv::SelectParams prm, long long units, long long max_blocks, cudaStream_t stream) {
+    auto kernel = pkv::select_blocks_kernel<D, TALL>;
+    const int dev = current_device();
+    static DeviceCache done{};
+    if (!allow_smem(kernel, done, dev)) return PKV_ECUDA;
+    int splits = 1;
+    while (splits < pkv::kSelMaxCluster && units * splits < 2ll * sm_count(dev) &&
+           max_blocks / (2 * splits) >= kSelectMinBlocks)
+        splits *= 2;
+    while (splits < pkv::kSelMaxCluster && select_smem((max_blocks + splits - 1) / splits) > kMaxDynamicSmem) splits *= 2;
+    prm.splits = splits;
+    prm.cap = (int)((max_blocks + splits - 1) / splits);
+    const size_t smem = select_smem(prm.cap);
+    if (smem > kMaxDynamicSmem || units * splits > 0x7fffffffll) return PKV_EUNSUPPORTED;
+    ClusterLaunch cl(units * splits, pkv::kSelThreads, smem, splits, stream);
+    if (cudaLaunchKernelEx(&cl.cfg, kernel, prm) != cudaSuccess) return PKV_ECUDA;
+    return launch_status();
 }
 
 // -------------------------------------------------------- prefill ----
@@ -801,6 +904,95 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
         else pkv::key_bounds_kernel<64, false><<<grid, threads, 0, st>>>(p);
     }
     return launch_status();
+}
+
+pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t num_kv_heads, pkv_pool pool, int32_t *selected,
+                             int32_t num_selected, int32_t max_context_len, pkv_stream_t stream) {
+    const pkv_status ps = check_pool(pool);
+    if (ps != PKV_OK) return ps;
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+        num_selected < 2)
+        return PKV_EINVAL;
+    if (num_kv_heads != pool.num_kv_heads || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+    const int g = num_q_heads / num_kv_heads;
+    if (g > 16) return PKV_EUNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !bounds || !block_tables || !context_lens || !selected) return PKV_EINVAL;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(selected, 4))
+        return PKV_EINVAL;
+    pkv::SelectParams p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.bounds = static_cast<const __nv_bfloat16 *>(bounds);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.selected = selected;
+    p.H = num_kv_heads;
+    p.g = g;
+    p.MBS = max_blocks_per_seq;
+    p.bs = pool.block_size;
+    p.NB = pool.num_blocks;
+    p.K = num_selected;
+    p.max_ctx = max_context_len;
+    const long long units = (long long)num_seqs * num_kv_heads;
+    const long long blocks = std::max<long long>(
+        1, std::min<long long>(max_blocks_per_seq, ((long long)max_context_len + pool.block_size - 1) / pool.block_size));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (pool.head_dim == 128)
+        return g > 8 ? launch_select<128, true>(p, units, blocks, st) : launch_select<128, false>(p, units, blocks, st);
+    return g > 8 ? launch_select<64, true>(p, units, blocks, st) : launch_select<64, false>(p, units, blocks, st);
+}
+
+pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                                    const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *context_lens, const int32_t *selected, int32_t num_selected,
+                                    int32_t num_seqs, int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out,
+                                    pkv_pool pool, pkv_stream_t stream) {
+    const pkv_status ps = check_pool(pool);
+    if (ps != PKV_OK) return ps;
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
+        return PKV_EINVAL;
+    if (num_kv_heads != pool.num_kv_heads || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+    const bool kv8 = pool.kv_dtype == PKV_KV_E4M3;
+    if (kv8 != (k_scales != nullptr) || kv8 != (v_scales != nullptr)) return PKV_EINVAL;
+    const int g = num_q_heads / num_kv_heads;
+    if (g > 16 || (long long)num_selected * pool.block_size >= (1ll << 31)) return PKV_EUNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !selected || !out) return PKV_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(selected, 4) || !aligned(k_scales, 4) ||
+        !aligned(v_scales, 4))
+        return PKV_EINVAL;
+    pkv::SparseParams p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.selected = selected;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.g = g;
+    p.MBS = max_blocks_per_seq;
+    p.bs = pool.block_size;
+    p.NB = pool.num_blocks;
+    p.K = num_selected;
+    p.pool_rows = pool.num_blocks * pool.num_kv_heads * pool.block_size;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    CUtensorMap mk, mv;
+    if (kv8) {
+        if (!encode_pool_map_u8(&mk, k_cache, pool) || !encode_pool_map_u8(&mv, v_cache, pool)) return PKV_ECUDA;
+    } else if (!encode_pool_map(&mk, k_cache, pool) || !encode_pool_map(&mv, v_cache, pool)) {
+        return PKV_ECUDA;
+    }
+    const long long units = (long long)num_seqs * num_kv_heads;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (pool.head_dim == 128)
+        return kv8 ? dispatch_sparse<128, true>(p, units, mk, mv, st) : dispatch_sparse<128, false>(p, units, mk, mv, st);
+    return kv8 ? dispatch_sparse<64, true>(p, units, mk, mv, st) : dispatch_sparse<64, false>(p, units, mk, mv, st);
 }
 
 size_t pkv_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

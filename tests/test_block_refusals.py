@@ -113,3 +113,41 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError):  # a transposed view
         pkv.pkv_write_fp8_block(k.transpose(0, 1), k, *[torch.zeros(1, dtype=i32)] * 3, *[torch.zeros((4, 2))] * 2,
                                 *[torch.zeros((4, 2, 16, 64), dtype=u8)] * 2, 1)
+
+
+def select(**kw):
+    a = dict(q=FAKE, bounds=FAKE, tables=FAKE, mbs=4, ctx=FAKE, B=2, Hq=4, Hkv=2, pool=pool(), sel=FAKE, K=4, max_ctx=64)
+    a.update(kw)
+    return pkv.load_library().pkv_select_blocks(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"B": 0}, 0), ({"B": -1}, EINVAL), ({"Hq": 5}, EINVAL), ({"Hq": 34}, EUNSUP), ({"Hkv": 4, "Hq": 8}, EINVAL),
+    ({"K": 1}, EINVAL), ({"K": 0}, EINVAL), ({"max_ctx": -1}, EINVAL), ({"mbs": 0}, EINVAL),
+    ({"pool": pool(d=96)}, EUNSUP), ({"pool": pool(bs=20)}, EUNSUP), ({"pool": pool(dtype=7)}, EINVAL),
+    *[({n: None}, EINVAL) for n in ("q", "bounds", "tables", "ctx", "sel")],
+    *[({n: ODD16}, EINVAL) for n in ("q", "bounds")],
+    *[({n: ODD4}, EINVAL) for n in ("tables", "ctx", "sel")],
+])
+def test_select_refuses(change, status):
+    assert select(**change) == status
+
+
+def sparse(**kw):
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, tables=FAKE, mbs=4, ctx=FAKE, sel=FAKE, K=4, B=2, Hq=4,
+             scale=0.1, Hkv=2, out=FAKE, pool=pool())
+    a.update(kw)
+    return pkv.load_library().paged_attn_decode_sparse(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"B": 0}, 0), ({"B": -1}, EINVAL), ({"Hq": 5}, EINVAL), ({"Hq": 34}, EUNSUP), ({"Hkv": 4, "Hq": 8}, EINVAL),
+    ({"K": 0}, EINVAL), ({"K": 1 << 27}, EUNSUP), ({"mbs": 0}, EINVAL), ({"pool": pool(d=256)}, EUNSUP),
+    ({"ks": None}, EINVAL), ({"vs": None}, EINVAL), ({"pool": pool(dtype=0)}, EINVAL),  # scales go with an e4m3 pool
+    ({"ks": None, "pool": pool(dtype=0)}, EINVAL), ({"pool": pool(dtype=3)}, EINVAL),
+    *[({n: None}, EINVAL) for n in ("q", "kc", "vc", "tables", "ctx", "sel", "out")],
+    *[({n: ODD16}, EINVAL) for n in ("q", "kc", "vc", "out")],
+    *[({n: ODD4}, EINVAL) for n in ("ks", "vs", "tables", "ctx", "sel")],
+])
+def test_sparse_decode_refuses(change, status):
+    assert sparse(**change) == status
