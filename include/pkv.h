@@ -332,11 +332,14 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  *     a    = the largest finite |x| of the rows it receives
  *     need = the least power of two >= 2^-126 with a <= 448 * need
  *     s'   = need if the block holds no older row, else max(scale, need)
- *     older rows: code = e4m3_rne(e4m3(code) * scale / s')   (unchanged if s' = scale)
  *     new rows:   code = e4m3_rne_satfinite(x / s')
- *   and s' becomes the block's scale.  Infinities saturate, NaN stays NaN.
- *   Rows past query_start[num_seqs] are not read; codes and scales of other
- *   blocks, and codes past a context, stay as they were.
+ *     the block's other rows, if it holds an older one and s' > scale:
+ *                 code = e4m3_rne(e4m3(code) * scale / s')
+ *   and s' becomes the block's scale.  (A grown scale takes the rows past the
+ *   context along, so every code of the block keeps its value as nearly as it
+ *   can.)  Infinities saturate, NaN stays NaN.  Rows past
+ *   query_start[num_seqs] are not read; codes and scales of other blocks, and
+ *   the other rows of a block whose scale does not grow, stay as they were.
  *     query_start     int32 [num_seqs + 1], non-decreasing
  *     max_new_tokens  host upper bound of the new tokens of a sequence
  *   Two sequences must not append to the same block (copy it first).  A
@@ -406,11 +409,13 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *     bounds    as pkv_key_bounds leaves it (pool gives its sizes; either kv_dtype)
  *     selected  int32 [num_seqs][num_kv_heads][num_selected], num_selected >= 2:
  *               ascending logical blocks, then -1
- *     max_context_len  host upper bound of context_lens; above 8 * 13000 blocks
- *               (or the table's length, if less) gives PKV_EUNSUPPORTED
+ *     max_context_len  host upper bound of context_lens (sizes the workspace;
+ *               above 800000 blocks: PKV_EUNSUPPORTED)
+ *     workspace  at least pkv_select_workspace_bytes(...), 256-B aligned, as in
+ *               paged_attn_decode
  *   A context length < 0 or above the table / max_context_len sets
  *   PKV_DEVERR_CONTEXT and is clamped; a block id outside the pool sets
- *   PKV_DEVERR_BLOCK and scores -infinity.  One kernel, no workspace.
+ *   PKV_DEVERR_BLOCK and scores -infinity.  Two kernels (scores, selection).
  *
  * paged_attn_decode_sparse: paged_attn_decode over the rows of the selected
  *   blocks that lie under the context: i runs over the positions of blocks
@@ -426,10 +431,14 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *   num_selected up to about 10000 blocks (more: PKV_EUNSUPPORTED).  One
  *   kernel, no workspace.
  */
+/* Device scratch of pkv_select_blocks; 0 for invalid sizes. */
+size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
+                                  int32_t max_context_len);
 pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *block_tables,
                              int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                              int32_t num_q_heads, int32_t num_kv_heads, pkv_pool pool, int32_t *selected,
-                             int32_t num_selected, int32_t max_context_len, pkv_stream_t stream);
+                             int32_t num_selected, int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                             pkv_stream_t stream);
 pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
                                     const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                     const int32_t *context_lens, const int32_t *selected, int32_t num_selected,

@@ -30,7 +30,8 @@ EXPORTED = ("pkv_write", "pkv_copy_blocks", "pkv_decode_workspace_bytes", "paged
             "pkv_bm_free", "pkv_bm_share", "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8",
             "paged_attn_decode_fp8", "pkv_prefix_cache_bytes", "pkv_prefix_cache_init", "pkv_prefix_lookup",
             "pkv_prefix_insert", "pkv_write_fp8_block", "pkv_copy_scales", "pkv_copy_scales_dev",
-            "paged_attn_decode_fp8_block", "pkv_key_bounds", "pkv_select_blocks", "paged_attn_decode_sparse")
+            "paged_attn_decode_fp8_block", "pkv_key_bounds", "pkv_select_workspace_bytes", "pkv_select_blocks",
+            "paged_attn_decode_sparse")
 STATIC_WS_BYTES = 32 << 20  # PKV_STATIC_WS_BYTES
 
 
@@ -89,7 +90,9 @@ def load_library() -> ctypes.CDLL:
         lib.pkv_copy_scales_dev.argtypes = [P, P, I32, P, P, I32, I32, P]
         lib.paged_attn_decode_fp8_block.argtypes = lib.paged_attn_decode_fp8.argtypes
         lib.pkv_key_bounds.argtypes = [P, P, P, I32, P, P, I32, I32, P, _Pool, P]
-        lib.pkv_select_blocks.argtypes = [P, P, P, I32, P, I32, I32, I32, _Pool, P, I32, I32, P]
+        lib.pkv_select_workspace_bytes.argtypes = [I32, I32, I32, I32]
+        lib.pkv_select_workspace_bytes.restype = SZ
+        lib.pkv_select_blocks.argtypes = [P, P, P, I32, P, I32, I32, I32, _Pool, P, I32, I32, P, SZ, P]
         lib.paged_attn_decode_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, I32, I32, F, I32, P, _Pool, P]
         lib.pkv_status_string.argtypes = [ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
@@ -448,23 +451,31 @@ def _need_append(block_tables, context_lens, query_start):
         raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B], query_start [B + 1]")
 
 
-class _one_device:
-    """Every tensor of a call on one GPU, and that GPU current while it runs."""
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, first: torch.Tensor, *others):
-        self.index = index = first.device.index
-        for t in others:
-            if t is not None and t.device.index != index:
-                raise ValueError("all tensors must be on one device")
-        self.previous = torch.cuda.current_device()
 
-    def __enter__(self):
-        if self.index != self.previous:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.index != self.previous:
-            torch.cuda.set_device(self.previous)
+def _launch(what: str, tensors, stream, f, *args) -> None:
+    """Calls f(*args, stream) with the tensors' GPU current (None among them: an absent argument); stream None: that
+    GPU's current stream."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{what}: all tensors must be on one device")
+    previous = _current_device()
+    if index != previous:
+        torch.cuda.set_device(index)
+    try:
+        if stream is None:
+            raw = _current_raw_stream(index)
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        status = f(*args, raw)
+    finally:
+        if index != previous:
+            torch.cuda.set_device(previous)
+    if status != PKV_OK:
+        raise PkvError(status, what)
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -491,22 +502,20 @@ def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Te
     T = k.shape[0]
     if k.shape != (T, k_cache.shape[1], k_cache.shape[3]) or v.shape != k.shape or v_cache.shape != k_cache.shape:
         raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim] and the caches alike")
-    with _one_device(k, v, block_tables, context_lens, query_start, k_scales, v_scales, k_cache, v_cache):
-        st = load_library().pkv_write_fp8_block(
-            k.data_ptr(), v.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-            query_start.data_ptr(), context_lens.shape[0], T, int(max_new_tokens), k_scales.data_ptr(),
-            v_scales.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _pool(k_cache), _stream(stream))
-    _check(st, "pkv_write_fp8_block")
+    _launch("pkv_write_fp8_block", (k, v, block_tables, context_lens, query_start, k_scales, v_scales, k_cache,
+            v_cache), stream, load_library().pkv_write_fp8_block, k.data_ptr(), v.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), context_lens.shape[0], T,
+            int(max_new_tokens), k_scales.data_ptr(), v_scales.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            _pool(k_cache))
 
 
 def pkv_copy_scales(src_dst_pairs, k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
     """Copies row src -> dst of both scale arrays for every (src, dst) host pair: pkv_copy_blocks' companion."""
     _need_scale_rows(k_scales, v_scales)
     pairs = np.ascontiguousarray(np.asarray(src_dst_pairs, dtype=np.int32).reshape(-1, 2))
-    with _one_device(k_scales, v_scales):
-        st = load_library().pkv_copy_scales(pairs.ctypes.data_as(ctypes.c_void_p), pairs.shape[0], _ptr(k_scales),
-                                            _ptr(v_scales), k_scales.shape[0], k_scales.shape[1], _stream(stream))
-    _check(st, "pkv_copy_scales")
+    _launch("pkv_copy_scales", (k_scales, v_scales), stream, load_library().pkv_copy_scales,
+            pairs.ctypes.data_as(ctypes.c_void_p), pairs.shape[0], _ptr(k_scales), _ptr(v_scales), k_scales.shape[0],
+            k_scales.shape[1])
 
 
 def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
@@ -516,10 +525,9 @@ def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: 
     _need(cow_pairs, "cow_pairs", torch.int32)
     _need(num_pairs, "num_pairs", torch.int32)
     _need_scale_rows(k_scales, v_scales)
-    with _one_device(k_scales, v_scales, cow_pairs, num_pairs):
-        st = load_library().pkv_copy_scales_dev(_ptr(cow_pairs), _ptr(num_pairs), cow_pairs.shape[0], _ptr(k_scales),
-                                                _ptr(v_scales), k_scales.shape[0], k_scales.shape[1], _stream(stream))
-    _check(st, "pkv_copy_scales_dev")
+    _launch("pkv_copy_scales_dev", (k_scales, v_scales, cow_pairs, num_pairs), stream,
+            load_library().pkv_copy_scales_dev, _ptr(cow_pairs), _ptr(num_pairs), cow_pairs.shape[0], _ptr(k_scales),
+            _ptr(v_scales), k_scales.shape[0], k_scales.shape[1])
 
 
 def _need_scale_rows(k_scales, v_scales):
@@ -550,13 +558,12 @@ def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if workspace is None:
         workspace = _scratch(decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens),
                              q.device, stream)
-    with _one_device(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, out, workspace):
-        st = load_library().paged_attn_decode_fp8_block(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale),
-            int(num_kv_heads), out.data_ptr(), _pool(k_cache), int(max_context_len), int(partition_tokens),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "paged_attn_decode_fp8_block")
+    _launch("paged_attn_decode_fp8_block", (q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+            out, workspace), stream, load_library().paged_attn_decode_fp8_block, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), int(num_kv_heads), out.data_ptr(),
+            _pool(k_cache), int(max_context_len), int(partition_tokens), workspace.data_ptr(), workspace.numel() *
+            workspace.element_size())
 
 
 def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -574,12 +581,10 @@ def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_le
         raise ValueError("k_scales belong to an e4m3 pool, and only there")
     if k_scales is not None:
         _need_block_scales(k_scales, k_scales, k_cache)
-    with _one_device(k_cache, block_tables, context_lens, query_start, bounds, k_scales):
-        st = load_library().pkv_key_bounds(
-            k_cache.data_ptr(), None if k_scales is None else k_scales.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), context_lens.shape[0],
-            int(max_new_tokens), bounds.data_ptr(), _pool(k_cache), _stream(stream))
-    _check(st, "pkv_key_bounds")
+    _launch("pkv_key_bounds", (k_cache, block_tables, context_lens, query_start, bounds, k_scales), stream,
+            load_library().pkv_key_bounds, k_cache.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(),
+            context_lens.shape[0], int(max_new_tokens), bounds.data_ptr(), _pool(k_cache))
 
 
 def _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads):
@@ -593,9 +598,16 @@ def _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads):
         raise ValueError("selected must be [B, num_kv_heads, num_selected]")
 
 
+def select_workspace_bytes(num_seqs: int, num_kv_heads: int, block_size: int, max_context_len: int) -> int:
+    n = load_library().pkv_select_workspace_bytes(num_seqs, num_kv_heads, block_size, max_context_len)
+    if n == 0:
+        raise ValueError("invalid sizes for the selection workspace")
+    return int(n)
+
+
 def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                       num_kv_heads: int, block_size: int, selected: torch.Tensor, max_context_len: int,
-                      stream=None) -> None:
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """selected[s][h] (int32 [B, num_kv_heads, K], K >= 2) := the logical blocks that decode attention of sequence s
     and kv head h keeps: the first, the last, and the best others by the upper bound of q.k that bounds
     (pkv_key_bounds) give, ascending; a context of at most K blocks keeps all, and -1 fills the row."""
@@ -604,12 +616,14 @@ def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch
     if bounds.dim() != 4 or bounds.shape[1:] != (num_kv_heads, 2, q.shape[2]):
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
     pool = _Pool(bounds.shape[0], bounds.shape[1], int(block_size), bounds.shape[3], KV_BF16)
-    with _one_device(q, bounds, block_tables, context_lens, selected):
-        st = load_library().pkv_select_blocks(
-            q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-            q.shape[0], q.shape[1], int(num_kv_heads), pool, selected.data_ptr(), selected.shape[2],
-            int(max_context_len), _stream(stream))
-    _check(st, "pkv_select_blocks")
+    if workspace is None:
+        workspace = _scratch(select_workspace_bytes(q.shape[0], num_kv_heads, block_size, max_context_len), q.device,
+                             stream)
+    _launch("pkv_select_blocks", (q, bounds, block_tables, context_lens, selected, workspace), stream,
+            load_library().pkv_select_blocks, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), q.shape[0], q.shape[1], int(num_kv_heads), pool,
+            selected.data_ptr(), selected.shape[2], int(max_context_len), workspace.data_ptr(), workspace.numel() *
+            workspace.element_size())
 
 
 def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -632,13 +646,11 @@ def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
         raise ValueError("k_scales and v_scales belong to an e4m3 pool, and only there")
     if fp8:
         _need_block_scales(k_scales, v_scales, k_cache)
-    with _one_device(q, k_cache, v_cache, block_tables, context_lens, selected, out, k_scales, v_scales):
-        st = load_library().paged_attn_decode_sparse(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
-            v_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
-            context_lens.data_ptr(), selected.data_ptr(), selected.shape[2], q.shape[0], q.shape[1], float(scale),
-            int(num_kv_heads), out.data_ptr(), _pool(k_cache), _stream(stream))
-    _check(st, "paged_attn_decode_sparse")
+    _launch("paged_attn_decode_sparse", (q, k_cache, v_cache, block_tables, context_lens, selected, out,
+            k_scales, v_scales), stream, load_library().paged_attn_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None, v_scales.data_ptr() if fp8 else None,
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(),
+            selected.shape[2], q.shape[0], q.shape[1], float(scale), int(num_kv_heads), out.data_ptr(), _pool(k_cache))
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -72,8 +72,8 @@ constexpr int kTouchTeams = 4;  // teams of one warp in a CTA
 //   a    = the largest finite |x| of the new rows
 //   need = the least power of two s >= 2^-126 with a <= 448 s
 //   s'   = need if no older row is held, else max(s, need)
-//   older rows: code' = e4m3(e4m3(code) s / s'), only when s' > s
 //   new rows:   code  = e4m3(x / s')
+//   all others: code' = e4m3(e4m3(code) s / s'), only when s' > s > 0
 // A power of two makes both products exact in fp32 (so each element is rounded
 // once, ties to even, saturating; fp32 underflow rounds to a zero code), and
 // growing a scale exact for every code that stays a normal e4m3 number.
@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
     }
     if (t.old > 0 && grown > s_old) {
         const float ratio = s_old * inv;
-        for (int row = wt * RPP + sub; row < t.old; row += p.W * RPP) {
+        for (int row = wt * RPP + sub; row < p.t.bs; row += p.W * RPP) {
+            if (row >= t.old && row < t.held) continue;
             uint2 w = cache[(size_t)row * VPR + c];
             w.x = rescale_codes(w.x, ratio);
             w.y = rescale_codes(w.y, ratio);

@@ -263,7 +263,7 @@ struct ClusterLaunch {
         attr[1].val.clusterDim.y = 1;
         attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 2;
+        cfg.numAttrs = splits > 1 ? 2 : 1;
     }
 };
 
@@ -319,27 +319,45 @@ pkv_status dispatch_sparse(const pkv::SparseParams &prm, long long units, const 
     return launch_sparse<D, 1, 16, KV8>(prm, units, mk, mv, stream);
 }
 
-constexpr int kSelectMinBlocks = 64;  // blocks of a CTA, below which a unit is not split further
+// Blocks of a (sequence, kv head) at most, and the parts of the workspace: the
+// scores, the error bounds, and the fp64 keys.
+struct SelectLayout {
+    long long blocks, stride, runs;
+    int run;
+    size_t off_errors, off_keys, total;
+};
 
-size_t select_smem(long long cap) { return (sizeof(pkv::SelectSmem) + 15) / 16 * 16 + (size_t)((cap + 3) / 4 * 4) * 16; }
+// Runs of two rounds of copies (fewer prologues), or of one when those are too
+// few to fill the SMs.
+bool select_layout(int32_t B, int32_t H, int32_t bs, int32_t max_ctx, int sms, SelectLayout *w) {
+    if (B < 0 || H <= 0 || bs <= 0 || max_ctx < 0) return false;
+    w->blocks = std::max<long long>(1, ((long long)max_ctx + bs - 1) / bs);
+    w->stride = (w->blocks + 31) / 32 * 32;
+    const long long rounds = (w->blocks + pkv::kScoreRound - 1) / pkv::kScoreRound;
+    w->run = pkv::kScoreRound * ((long long)B * H * rounds > 6ll * sms ? 2 : 1);
+    w->runs = (w->blocks + w->run - 1) / w->run;
+    const size_t units = (size_t)B * H;
+    w->off_errors = round256(units * w->stride * sizeof(float));
+    // (sized for runs of one round, so that it does not depend on the GPU)
+    w->off_keys = w->off_errors + round256(units * rounds * sizeof(float));
+    w->total = w->off_keys + round256(units * w->stride * sizeof(uint64_t));
+    return true;
+}
 
-template <int D, bool TALL>
-pkv_status launch_select(pkv::SelectParams prm, long long units, long long max_blocks, cudaStream_t stream) {
-    auto kernel = pkv::select_blocks_kernel<D, TALL>;
+template <int D>
+pkv_status launch_select(const pkv::SelectParams &p, long long units, cudaStream_t stream) {
     const int dev = current_device();
-    static DeviceCache done{};
-    if (!allow_smem(kernel, done, dev)) return PKV_ECUDA;
-    int splits = 1;
-    while (splits < pkv::kSelMaxCluster && units * splits < 2ll * sm_count(dev) &&
-           max_blocks / (2 * splits) >= kSelectMinBlocks)
-        splits *= 2;
-    while (splits < pkv::kSelMaxCluster && select_smem((max_blocks + splits - 1) / splits) > kMaxDynamicSmem) splits *= 2;
-    prm.splits = splits;
-    prm.cap = (int)((max_blocks + splits - 1) / splits);
-    const size_t smem = select_smem(prm.cap);
-    if (smem > kMaxDynamicSmem || units * splits > 0x7fffffffll) return PKV_EUNSUPPORTED;
-    ClusterLaunch cl(units * splits, pkv::kSelThreads, smem, splits, stream);
-    if (cudaLaunchKernelEx(&cl.cfg, kernel, prm) != cudaSuccess) return PKV_ECUDA;
+    static DeviceCache done_score{}, done_tall{}, done_select{};
+    const bool tall = p.g > 8;
+    auto score = tall ? pkv::score_blocks_kernel<D, true> : pkv::score_blocks_kernel<D, false>;
+    auto select = pkv::select_blocks_kernel<D>;
+    if (!allow_smem(score, tall ? done_tall : done_score, dev) || !allow_smem(select, done_select, dev)) return PKV_ECUDA;
+    const size_t smem = sizeof(pkv::SelectSmem) + (size_t)p.stride / 32 * 8;
+    if (smem > kMaxDynamicSmem || units * p.runs > 0x7fffffffll) return PKV_EUNSUPPORTED;
+    ClusterLaunch sc(units * p.runs, pkv::kScoreWarps * 32, pkv::ScoreSmem<D>::kAlloc, 1, stream);
+    if (cudaLaunchKernelEx(&sc.cfg, score, p) != cudaSuccess) return PKV_ECUDA;
+    ClusterLaunch se(units, pkv::kSelThreads, smem, 1, stream);
+    if (cudaLaunchKernelEx(&se.cfg, select, p) != cudaSuccess) return PKV_ECUDA;
     return launch_status();
 }
 
@@ -906,10 +924,17 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
     return launch_status();
 }
 
+size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
+                                  int32_t max_context_len) {
+    SelectLayout w;
+    return select_layout(num_seqs, num_kv_heads, block_size, max_context_len, 148, &w) ? w.total : 0;
+}
+
 pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *block_tables,
                              int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                              int32_t num_q_heads, int32_t num_kv_heads, pkv_pool pool, int32_t *selected,
-                             int32_t num_selected, int32_t max_context_len, pkv_stream_t stream) {
+                             int32_t num_selected, int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                             pkv_stream_t stream) {
     const pkv_status ps = check_pool(pool);
     if (ps != PKV_OK) return ps;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
@@ -919,9 +944,13 @@ pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *b
     const int g = num_q_heads / num_kv_heads;
     if (g > 16) return PKV_EUNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
-    if (!q || !bounds || !block_tables || !context_lens || !selected) return PKV_EINVAL;
+    if (!q || !bounds || !block_tables || !context_lens || !selected || !workspace) return PKV_EINVAL;
     if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
-        !aligned(selected, 4))
+        !aligned(selected, 4) || !aligned(workspace, 256))
+        return PKV_EINVAL;
+    SelectLayout wl;
+    if (!select_layout(num_seqs, num_kv_heads, pool.block_size, max_context_len, sm_count(current_device()), &wl) ||
+        workspace_bytes < wl.total)
         return PKV_EINVAL;
     pkv::SelectParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -936,13 +965,16 @@ pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *b
     p.NB = pool.num_blocks;
     p.K = num_selected;
     p.max_ctx = max_context_len;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.scores = reinterpret_cast<float *>(ws);
+    p.errors = reinterpret_cast<float *>(ws + wl.off_errors);
+    p.keys = reinterpret_cast<uint64_t *>(ws + wl.off_keys);
+    p.run = wl.run;
+    p.runs = (int)wl.runs;
+    p.stride = (int)wl.stride;
     const long long units = (long long)num_seqs * num_kv_heads;
-    const long long blocks = std::max<long long>(
-        1, std::min<long long>(max_blocks_per_seq, ((long long)max_context_len + pool.block_size - 1) / pool.block_size));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (pool.head_dim == 128)
-        return g > 8 ? launch_select<128, true>(p, units, blocks, st) : launch_select<128, false>(p, units, blocks, st);
-    return g > 8 ? launch_select<64, true>(p, units, blocks, st) : launch_select<64, false>(p, units, blocks, st);
+    return pool.head_dim == 128 ? launch_select<128>(p, units, st) : launch_select<64>(p, units, st);
 }
 
 pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,

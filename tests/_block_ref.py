@@ -42,7 +42,7 @@ def write(codes, scales, x, tables, ctx, start, bs):
                     was = scales[blk, h]
                     need = max(was, need)
                     if need > was:
-                        codes[blk, h, :old] = oracle.e4m3_encode(oracle.e4m3_decode(codes[blk, h, :old]) * (was / need))
+                        codes[blk, h] = oracle.e4m3_encode(oracle.e4m3_decode(codes[blk, h]) * (was / need))
                 codes[blk, h, old:held] = oracle.e4m3_encode(rows / need)
                 scales[blk, h] = need
             j += 1

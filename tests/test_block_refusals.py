@@ -116,7 +116,8 @@ def test_binding_refuses_wrong_tensors():
 
 
 def select(**kw):
-    a = dict(q=FAKE, bounds=FAKE, tables=FAKE, mbs=4, ctx=FAKE, B=2, Hq=4, Hkv=2, pool=pool(), sel=FAKE, K=4, max_ctx=64)
+    a = dict(q=FAKE, bounds=FAKE, tables=FAKE, mbs=4, ctx=FAKE, B=2, Hq=4, Hkv=2, pool=pool(), sel=FAKE, K=4, max_ctx=64,
+             ws=FAKE, ws_bytes=1 << 20)
     a.update(kw)
     return pkv.load_library().pkv_select_blocks(*a.values(), None)
 
@@ -125,7 +126,8 @@ def select(**kw):
     ({"B": 0}, 0), ({"B": -1}, EINVAL), ({"Hq": 5}, EINVAL), ({"Hq": 34}, EUNSUP), ({"Hkv": 4, "Hq": 8}, EINVAL),
     ({"K": 1}, EINVAL), ({"K": 0}, EINVAL), ({"max_ctx": -1}, EINVAL), ({"mbs": 0}, EINVAL),
     ({"pool": pool(d=96)}, EUNSUP), ({"pool": pool(bs=20)}, EUNSUP), ({"pool": pool(dtype=7)}, EINVAL),
-    *[({n: None}, EINVAL) for n in ("q", "bounds", "tables", "ctx", "sel")],
+    ({"ws_bytes": 16}, EINVAL), ({"ws": ODD16}, EINVAL),
+    *[({n: None}, EINVAL) for n in ("q", "bounds", "tables", "ctx", "sel", "ws")],
     *[({n: ODD16}, EINVAL) for n in ("q", "bounds")],
     *[({n: ODD4}, EINVAL) for n in ("tables", "ctx", "sel")],
 ])

@@ -74,6 +74,17 @@ def test_write_growth_and_special_values(D):
     no_device_error()
 
 
+def test_write_grows_a_block_whole():
+    """Rows past the context keep their values too when the scale of their block grows, NaN among them."""
+    b = ref.Batch([20, 35], [1, 2], 2, 128, 16, seed=15)
+    b.ks[:], b.vs[:] = 2.0 ** -9, 2.0 ** -5
+    b.kc[b.tables[0, 1], :, 9] = 0x7F
+    got = run_write(b, k=b.k * 50, v=b.v * 1e4)
+    check_write(b, got, k=b.k * 50, v=b.v * 1e4)
+    assert (got[2] > b.ks).sum() == 4 and (got[0][b.tables[0, 1], :, 10:] != b.kc[b.tables[0, 1], :, 10:]).any()
+    no_device_error()
+
+
 def test_write_again_changes_nothing():
     """The same append on its own result: scales and codes stay (it is what a replayed graph does)."""
     b = ref.Batch([40, 9, 100], [5, 1, 100], 3, 128, 16, seed=8)

@@ -30,7 +30,7 @@ def random_bounds(b, seed, spread=1.0):
 def run_select(b, bounds, K, max_ctx=None, q=None, stream=None):
     sel = torch.full((len(b.ctx), b.H, K), -7, dtype=torch.int32, device="cuda")
     pkv.pkv_select_blocks(cuda(b.q if q is None else q), cuda(bounds), cuda(b.tables), cuda(b.ctx), b.H, b.bs, sel,
-                          int(max(b.ctx)) if max_ctx is None else max_ctx, stream)
+                          int(max(b.ctx)) if max_ctx is None else max_ctx, stream=stream)
     torch.cuda.synchronize()
     return sel.cpu().numpy()
 
