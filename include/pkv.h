@@ -354,13 +354,15 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  *   PKV_DEVERR_BLOCK and are skipped).
  *
  * paged_attn_decode_fp8_block: paged_attn_decode over this pool, at head
- *   dimensions 64 and 128 and every GQA group <= 16.  Scales are finite and
+ *   dimensions 64 and 128 and every GQA group <= 16, without a partition size:
+ *   the work of all sequences is divided evenly over the GPU.  Scales are finite and
  *   above zero for the blocks under a context.  The codes and q (divided by a
  *   power of two for each head) are multiplied as f16 with fp32 accumulation;
  *   a softmax weight times its block's V scale enters the weighted sum as f16,
  *   relative to the largest such product so far, whatever the scales' range
  *   (so one below 2^-14 of it is rounded to 2^-24 of it).
- *   The workspace is the same as paged_attn_decode's.
+ *   The workspace (pkv_decode_fp8_block_workspace_bytes, 256-B aligned) is used
+ *   as paged_attn_decode's.  Two kernels (attention, merge).
  */
 pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
@@ -374,8 +376,10 @@ pkv_status paged_attn_decode_fp8_block(const void *q, const void *k_cache, const
                                        const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
                                        int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
-                                       int32_t partition_tokens, void *workspace, size_t workspace_bytes,
-                                       pkv_stream_t stream);
+                                       void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+/* Device scratch of paged_attn_decode_fp8_block; 0 for invalid sizes. */
+size_t pkv_decode_fp8_block_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_context_len);
 
 /*
  * Block-sparse decode -- a decode step over a long context reads only the
@@ -427,9 +431,10 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *               (or an empty context) gives a zero output row.
  *     k_scales, v_scales  NULL for a bf16 pool; the block scales of an e4m3 pool
  *   Both pools at head dimensions 64 and 128 and every GQA group <= 16, with
- *   the arithmetic of paged_attn_decode and paged_attn_decode_fp8_block.
- *   num_selected up to about 10000 blocks (more: PKV_EUNSUPPORTED).  One
- *   kernel, no workspace.
+ *   fp32 sums; the weights enter the weighted sum rounded to 17 bits over a
+ *   bf16 pool, and as in paged_attn_decode_fp8_block over an e4m3 pool.  The
+ *   workspace (pkv_decode_sparse_workspace_bytes, 256-B aligned) is used as
+ *   paged_attn_decode's.  Two kernels (attention, merge).
  */
 /* Device scratch of pkv_select_blocks; 0 for invalid sizes. */
 size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
@@ -443,7 +448,10 @@ pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const vo
                                     const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                     const int32_t *context_lens, const int32_t *selected, int32_t num_selected,
                                     int32_t num_seqs, int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out,
-                                    pkv_pool pool, pkv_stream_t stream);
+                                    pkv_pool pool, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+/* Device scratch of paged_attn_decode_sparse; 0 for invalid sizes. */
+size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int32_t num_selected);
 
 /*
  * Block manager on the device -- the bookkeeping of the pages' block manager

@@ -30,7 +30,8 @@ EXPORTED = ("pkv_write", "pkv_copy_blocks", "pkv_decode_workspace_bytes", "paged
             "pkv_bm_free", "pkv_bm_share", "pkv_bm_append_slots", "pkv_copy_blocks_dev", "pkv_write_fp8",
             "paged_attn_decode_fp8", "pkv_prefix_cache_bytes", "pkv_prefix_cache_init", "pkv_prefix_lookup",
             "pkv_prefix_insert", "pkv_write_fp8_block", "pkv_copy_scales", "pkv_copy_scales_dev",
-            "paged_attn_decode_fp8_block", "pkv_key_bounds", "pkv_select_workspace_bytes", "pkv_select_blocks",
+            "paged_attn_decode_fp8_block", "pkv_decode_fp8_block_workspace_bytes", "pkv_key_bounds",
+            "pkv_select_workspace_bytes", "pkv_select_blocks", "pkv_decode_sparse_workspace_bytes",
             "paged_attn_decode_sparse")
 STATIC_WS_BYTES = 32 << 20  # PKV_STATIC_WS_BYTES
 
@@ -88,12 +89,16 @@ def load_library() -> ctypes.CDLL:
         lib.pkv_write_fp8_block.argtypes = [P, P, P, I32, P, P, I32, I32, I32, P, P, P, P, _Pool, P]
         lib.pkv_copy_scales.argtypes = [P, I32, P, P, I32, I32, P]
         lib.pkv_copy_scales_dev.argtypes = [P, P, I32, P, P, I32, I32, P]
-        lib.paged_attn_decode_fp8_block.argtypes = lib.paged_attn_decode_fp8.argtypes
+        lib.paged_attn_decode_fp8_block.argtypes = [P, P, P, P, P, P, I32, P, I32, I32, F, I32, P, _Pool, I32, P, SZ, P]
+        lib.pkv_decode_fp8_block_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+        lib.pkv_decode_fp8_block_workspace_bytes.restype = SZ
         lib.pkv_key_bounds.argtypes = [P, P, P, I32, P, P, I32, I32, P, _Pool, P]
         lib.pkv_select_workspace_bytes.argtypes = [I32, I32, I32, I32]
         lib.pkv_select_workspace_bytes.restype = SZ
         lib.pkv_select_blocks.argtypes = [P, P, P, I32, P, I32, I32, I32, _Pool, P, I32, I32, P, SZ, P]
-        lib.paged_attn_decode_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, I32, I32, F, I32, P, _Pool, P]
+        lib.paged_attn_decode_sparse.argtypes = [P, P, P, P, P, P, I32, P, P, I32, I32, I32, F, I32, P, _Pool, P, SZ, P]
+        lib.pkv_decode_sparse_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+        lib.pkv_decode_sparse_workspace_bytes.restype = SZ
         lib.pkv_status_string.argtypes = [ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
         lib.pkv_version.restype = I32
@@ -537,11 +542,19 @@ def _need_scale_rows(k_scales, v_scales):
         raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
 
 
+def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_context_len: int) -> int:
+    n = load_library().pkv_decode_fp8_block_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                            max_context_len)
+    if n == 0:
+        raise ValueError("invalid sizes for the decode workspace")
+    return int(n)
+
+
 def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
                                 v_scales: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                                 scale: float, num_kv_heads: int, out: torch.Tensor, max_context_len: int,
-                                partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
-                                stream=None) -> None:
+                                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_attn_decode over an FP8 (e4m3) pool with a K and a V scale for each (block, kv head)."""
     for t, n in ((q, "q"), (out, "out")):
         _need(t, n, torch.bfloat16)
@@ -556,14 +569,12 @@ def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
     if workspace is None:
-        workspace = _scratch(decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens),
-                             q.device, stream)
+        workspace = _scratch(decode_fp8_block_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len), q.device, stream)
     _launch("paged_attn_decode_fp8_block", (q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
             out, workspace), stream, load_library().paged_attn_decode_fp8_block, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
             block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), int(num_kv_heads), out.data_ptr(),
-            _pool(k_cache), int(max_context_len), int(partition_tokens), workspace.data_ptr(), workspace.numel() *
-            workspace.element_size())
+            _pool(k_cache), int(max_context_len), workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -626,11 +637,20 @@ def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch
             workspace.element_size())
 
 
+def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                  num_selected: int) -> int:
+    n = load_library().pkv_decode_sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                         num_selected)
+    if n == 0:
+        raise ValueError("invalid sizes for the decode workspace")
+    return int(n)
+
+
 def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                              block_tables: torch.Tensor, context_lens: torch.Tensor, selected: torch.Tensor,
                              scale: float, num_kv_heads: int, out: torch.Tensor,
                              k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
-                             stream=None) -> None:
+                             workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_attn_decode over the rows of the logical blocks selected[s][h] (negative entries: none) that lie under
     the context.  A bf16 pool, or an e4m3 pool with its block scales."""
     _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads)
@@ -646,11 +666,16 @@ def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
         raise ValueError("k_scales and v_scales belong to an e4m3 pool, and only there")
     if fp8:
         _need_block_scales(k_scales, v_scales, k_cache)
-    _launch("paged_attn_decode_sparse", (q, k_cache, v_cache, block_tables, context_lens, selected, out,
-            k_scales, v_scales), stream, load_library().paged_attn_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
+    B, Hq, D = q.shape
+    if workspace is None:
+        workspace = _scratch(decode_sparse_workspace_bytes(B, Hq, num_kv_heads, D, k_cache.shape[2], selected.shape[2]),
+                             q.device, stream)
+    _launch("paged_attn_decode_sparse", (q, k_cache, v_cache, block_tables, context_lens, selected, out, k_scales,
+            v_scales, workspace), stream, load_library().paged_attn_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None, v_scales.data_ptr() if fp8 else None,
             block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(),
-            selected.shape[2], q.shape[0], q.shape[1], float(scale), int(num_kv_heads), out.data_ptr(), _pool(k_cache))
+            selected.shape[2], B, Hq, float(scale), int(num_kv_heads), out.data_ptr(), _pool(k_cache),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

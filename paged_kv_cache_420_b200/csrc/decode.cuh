@@ -61,8 +61,6 @@ struct DecodeParams {
     float scale_log2;             // scale * log2(e)
     const float *k_scale = nullptr;  // FP8 pool: dequantisation scale per kv head (nullptr: bf16 pool)
     const float *v_scale = nullptr;
-    const float *kb_scales = nullptr;  // FP8 pool with a scale for each block: [NB][Hkv] (nullptr: none)
-    const float *vb_scales = nullptr;
 };
 
 // A context length clamped to what the table and the workspace can hold.  A
@@ -255,13 +253,12 @@ struct ItemMeta {
     }
 };
 
-template <int D, int GP, int NS, bool KV8 = false, bool KVB = false>
+template <int D, int GP, int NS, bool KV8 = false>
 struct DecodeSmem {
     static constexpr int kW = kConsumerWarps;
     static constexpr int kElem = KV8 ? 1 : 2;             // bytes per K/V element (e4m3 or bf16)
-    static constexpr int kBoxRow = D * kElem < 128 ? D * kElem : 128;  // bytes of a box row
-    static constexpr int kHalfTile = kStageTok * kBoxRow;  // one TMA box: 16 rows (2 KB at 128 bytes)
-    static constexpr int kBoxes = D * kElem / kBoxRow;     // boxes per row of a tile
+    static constexpr int kHalfTile = kStageTok * 128;     // one TMA box: 16 rows x 128 bytes = 2 KB
+    static constexpr int kBoxes = D * kElem / 128;        // boxes per row of a tile
     static constexpr int kTile = kStageTok * D * kElem;   // one K (or V) stage tile
     static constexpr int kStage = 2 * kTile;
     static constexpr int kQBuf = GP * D * 2;              // the query heads of one kv head
@@ -275,8 +272,7 @@ struct DecodeSmem {
     static constexpr int kNumBars = 2 * NS + 6;  // full, empty, qfull[2], qempty[2], mfull, mempty
     static constexpr int oInfo = oBars + kNumBars * 8;
     static constexpr int oAbort = oInfo + NS * (int)sizeof(StageInfo);
-    static constexpr int oScales = oAbort + 16;  // KVB: (K scale, V scale) of the block each slot's stage is in
-    static constexpr int kBytes = oScales + (KVB ? NS * 8 : 0);
+    static constexpr int kBytes = oAbort + 16;
     static constexpr int kAlloc = kBytes;  // the dynamic window is 1 KB-aligned (checked in the kernel)
 };
 
@@ -331,27 +327,10 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t tile, int r, int c) {
 }
 
 // Byte address of e4m3 element (row r, column c) of an FP8 stage tile: one
-// 128-byte line per row at head dim 128, 16-byte chunks XOR-swizzled with
-// (r & 7); two 64-byte rows per line at 64, chunks XOR-swizzled with the line.
-template <int D>
+// 128-byte line per row, 16-byte chunks XOR-swizzled with (r & 7).
 __device__ __forceinline__ uint32_t tile_addr8(uint32_t tile, int r, int c) {
-    if constexpr (D == 64) return tile + r * 64 + ((((c >> 4) ^ ((r >> 1) & 3))) << 4) + (c & 15);
     return tile + r * 128 + ((((c >> 4) ^ (r & 7))) << 4) + (c & 15);
 }
-
-// The power of two that brings a largest magnitude into [1, 2) (1/2 .. 4 at
-// the ends of the range): q is converted to f16 with it, so its elements keep
-// 11 bits down to 2^-14 of the head's largest whatever their size.  The
-// inverse, for the scores, is exact too.
-__device__ __forceinline__ void unit_power(float amax, float &down, float &up) {
-    const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
-    down = __uint_as_float((uint32_t)(254 - e) << 23);
-    up = __uint_as_float((uint32_t)e << 23);
-}
-
-// A block's V scale as an exponent.  A scale that is not above zero never
-// holds a value: its exponent is below every other's, and finite.
-__device__ __forceinline__ float scale_exponent(float vs) { return vs > 0.f ? __log2f(vs) : -1000.f; }
 
 // The two code pairs of a word of four e4m3 codes as f16x2 words: lo from
 // bytes 0-1, hi from bytes 2-3 (the halves are taken from the register as
@@ -391,30 +370,19 @@ __device__ __forceinline__ float fma_f16hi(uint32_t a, uint32_t b, float acc) {
 // KV8: the stage tiles hold e4m3 codes.  q is kept as exact f16 pairs, K and V
 // codes are converted to f16 (exactly) and multiplied in mixed precision with
 // fp32 accumulation; the K scale times scale * log2 e multiplies each summed
-// score, and the V scale is applied to the final output.  At head dim 64 a row
-// of codes takes 16 lanes, so the half-warps take the even and the odd tokens.
-// KVB: each stage lies in one block and has its own scales.  The K scale
-// multiplies the summed scores as before.  The V scale is a part of a token's
-// weight, 2^(z - m) vs, and blocks may differ in it by any power of two, while
-// the weight is used as f16: so the accumulator has a running reference of its
-// own, m2 ~ max(z + log2 vs), and holds sum 2^(z + log2 vs - m2) code, beside
-// m and l of the softmax.  Per stage that is one more exponential, 2^(m + log2
-// vs - m2), that multiplies every weight of the stage.
-template <int D, bool KV8 = false, bool KVB = false>
+// score, and the V scale is applied to the final output.
+template <int D, bool KV8 = false>
 struct SimtState {
-    static constexpr bool kHalf = KV8 && D == 64;
-    static constexpr int EPL = kHalf ? 4 : D / 32;  // elements per lane
+    static constexpr int EPL = D / 32;  // elements per lane
     float q[EPL];
     uint32_t q16[EPL / 2];  // KV8: q as f16 pairs
     float kscale;           // KV8: scale * log2(e) * k_scale of the kv head
     float acc[EPL];
     float m;
-    float m2;      // KVB: reference of acc
     float l_part;  // this lane's share of l
 
     __device__ __forceinline__ void reset() {
         m = PKV_NEG_INF;
-        m2 = PKV_NEG_INF;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
         l_part = 0.f;
@@ -422,30 +390,14 @@ struct SimtState {
 
     __device__ __forceinline__ void load_q(const __nv_bfloat16 *qs, int lane, float scale_log2) {
         kscale = scale_log2;
-        if constexpr (KVB) {
-            float x[EPL], amax = 0.f;
 #pragma unroll
-            for (int e = 0; e < EPL; e += 2) {
-                const uint32_t pr = *reinterpret_cast<const uint32_t *>(qs + (kHalf ? lane & 15 : lane) * EPL + e);
-                x[e] = bf16lo_to_f32(pr);
-                x[e + 1] = bf16hi_to_f32(pr);
-                amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
-            }
-            float down, up;
-            unit_power(warp_max_f32(amax), down, up);
-            kscale *= up;
-#pragma unroll
-            for (int e = 0; e < EPL; e += 2) q16[e / 2] = f16x2_from_f32(x[e] * down, x[e + 1] * down);
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPL; e += 2) {
-                const uint32_t pr = *reinterpret_cast<const uint32_t *>(qs + lane * EPL + e);
-                if constexpr (KV8) {
-                    q16[e / 2] = f16x2_from_f32(bf16lo_to_f32(pr), bf16hi_to_f32(pr));
-                } else {
-                    q[e] = bf16lo_to_f32(pr) * scale_log2;
-                    q[e + 1] = bf16hi_to_f32(pr) * scale_log2;
-                }
+        for (int e = 0; e < EPL; e += 2) {
+            const uint32_t pr = *reinterpret_cast<const uint32_t *>(qs + lane * EPL + e);
+            if constexpr (KV8) {
+                q16[e / 2] = f16x2_from_f32(bf16lo_to_f32(pr), bf16hi_to_f32(pr));
+            } else {
+                q[e] = bf16lo_to_f32(pr) * scale_log2;
+                q[e + 1] = bf16hi_to_f32(pr) * scale_log2;
             }
         }
     }
@@ -453,9 +405,7 @@ struct SimtState {
     // KV8: this lane's 4 codes of row r as two f16 pairs.
     __device__ __forceinline__ void load_row8(uint32_t tile, int r, int lane, uint32_t (&h)[2]) {
         uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];"
-                     : "=r"(w)
-                     : "r"(tile_addr8<D>(tile, r, (kHalf ? lane & 15 : lane) * EPL)));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(tile_addr8(tile, r, lane * EPL)));
         f16x2_from_e4m3x4(w, h[0], h[1]);
     }
 
@@ -475,21 +425,17 @@ struct SimtState {
     }
 
     // PARTIAL: fewer than 16 valid tokens in the stage (see MmaState::stage).
-    // ks, vs: the scales of the stage's block (KVB).
     template <bool PARTIAL>
-    __device__ __forceinline__ void stage(uint32_t ktile, uint32_t vtile, int valid, int lane, float ks = 1.f,
-                                          float vs = 1.f) {
-        constexpr int NV = kHalf ? 8 : 16;  // rows that a lane takes
-        const int half = kHalf ? lane >> 4 : 0;
-        float v[NV];
+    __device__ __forceinline__ void stage(uint32_t ktile, uint32_t vtile, int valid, int lane) {
+        float v[16];
         // q.k partial sums v[r] of token r; tokens r and r+1 share one packed
         // fp32x2 FMA per element.
         if constexpr (KV8) {
-            static_assert(EPL == 4, "a lane owns four codes of a row");
+            static_assert(EPL == 4, "FP8 stage tiles are 128-byte rows (head dim 128)");
 #pragma unroll
-            for (int r = 0; r < NV; ++r) {
+            for (int r = 0; r < 16; ++r) {
                 uint32_t k16[2];
-                load_row8(ktile, kHalf ? 2 * r + half : r, lane, k16);
+                load_row8(ktile, r, lane, k16);
                 float d = fma_f16lo(q16[0], k16[0], 0.f);
                 d = fma_f16hi(q16[0], k16[0], d);
                 d = fma_f16lo(q16[1], k16[1], d);
@@ -497,7 +443,7 @@ struct SimtState {
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < NV; r += 2) {
+            for (int r = 0; r < 16; r += 2) {
                 float x0[EPL], x1[EPL];
                 load_row(ktile, r, lane, x0);
                 load_row(ktile, r + 1, lane, x1);
@@ -510,16 +456,15 @@ struct SimtState {
         }
         // Transposing butterfly: each step halves the values a lane keeps and
         // sums its half with the partner's; after it lanes 2t and 2t+1 both
-        // hold the full 32-lane sum of token t (kHalf: the 16-lane sum of
-        // token 2 (t % 8) + half).
-        int n = NV;
+        // hold the full 32-lane sum of token t.
+        int n = 16;
 #pragma unroll
-        for (int mask = NV; mask >= 1; mask >>= 1) {
+        for (int mask = 16; mask >= 1; mask >>= 1) {
             if (n > 1) {
                 const bool upper = (lane & mask) != 0;
                 n >>= 1;
 #pragma unroll
-                for (int i = 0; i < NV / 2; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     if (i < n) {
                         const float send = upper ? v[i] : v[i + n];
                         const float keep = upper ? v[i + n] : v[i];
@@ -530,52 +475,26 @@ struct SimtState {
                 v[0] += __shfl_xor_sync(0xffffffffu, v[0], mask);
             }
         }
-        const int my_tok = kHalf ? 2 * ((lane >> 1) & 7) + half : lane >> 1;
-        const float kfac = KVB ? kscale * ks : kscale;
-        const float score = (!PARTIAL || my_tok < valid) ? (KV8 ? v[0] * kfac : v[0]) : PKV_NEG_INF;
+        const int my_tok = lane >> 1;
+        const float score = (!PARTIAL || my_tok < valid) ? (KV8 ? v[0] * kscale : v[0]) : PKV_NEG_INF;
         // stage max (one warp reduction), lazy rescale
         const float mx = warp_max_f32(score);
         if (mx > m + kRescaleSlack) {  // warp-uniform, rare after the first stage
             const float alpha = exp2f(m - mx);
             m = mx;
-            if constexpr (!KVB) {
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) acc[e] *= alpha;
-            }
+            for (int e = 0; e < EPL; ++e) acc[e] *= alpha;
             l_part *= alpha;
         }
-        float pr = exp2f(score - m);
+        const float pr = exp2f(score - m);
         l_part += pr;
-        if constexpr (KVB) {
-            const float lv = scale_exponent(vs);
-            const float my = mx + lv;
-            if (my > m2 + kRescaleSlack) {
-                const float alpha = exp2f(m2 - my);
-                m2 = my;
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) acc[e] *= alpha;
-            }
-            // the bound keeps 0 * infinity out; it is reached only by weights
-            // below 2^-118 of the largest
-            pr *= exp2f(fminf(m + lv - m2, 126.f));
-        }
         // KV8: p as an f16 pair, converted once here and shuffled as such
         const uint32_t pr16 = KV8 ? f16x2_from_f32(pr, pr) : 0u;
         // PV: broadcast p of each valid token (from lane 2r), accumulate its V
         // row (packed fp32x2 FMA over element pairs)
 #pragma unroll
-        for (int r = 0; r < NV; ++r) {
-            if constexpr (kHalf) {
-                const int row = 2 * r + half;
-                uint32_t v16[2];
-                load_row8(vtile, row, lane, v16);
-                if (PARTIAL && row >= valid) v16[0] = v16[1] = 0u;
-                const uint32_t p16 = __shfl_sync(0xffffffffu, pr16, (lane & 16) + 2 * r);
-                acc[0] = fma_f16lo(p16, v16[0], acc[0]);
-                acc[1] = fma_f16hi(p16, v16[0], acc[1]);
-                acc[2] = fma_f16lo(p16, v16[1], acc[2]);
-                acc[3] = fma_f16hi(p16, v16[1], acc[3]);
-            } else if (!PARTIAL || r < valid) {
+        for (int r = 0; r < 16; ++r) {
+            if (!PARTIAL || r < valid) {
                 if constexpr (KV8) {
                     uint32_t v16[2];
                     load_row8(vtile, r, lane, v16);
@@ -601,22 +520,8 @@ struct SimtState {
         float l = l_part;
 #pragma unroll
         for (int o = 2; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if constexpr (KVB) {  // from reference m2 to m
-            const float f = m2 == PKV_NEG_INF ? 0.f : exp2f(m2 - m);
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) acc[e] *= f;
-        }
-        if constexpr (kHalf) {
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
-            if (lane < 16) {
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) mO[w * stride + lane * EPL + e] = acc[e];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) mO[w * stride + lane * EPL + e] = acc[e];
-        }
+        for (int e = 0; e < EPL; ++e) mO[w * stride + lane * EPL + e] = acc[e];
         if (lane == 0) { mM[w] = m; mL[w] = l; }
     }
 };
@@ -650,9 +555,7 @@ __device__ __forceinline__ int perm16(int r) {
 //   V: one 8-bit transposing load per 16 head-dim columns gives lane l the
 //      codes of tokens 4j .. 4j+3 at columns l/4 and l/4 + 8, which in perm16
 //      order are exactly its A fragment of V^T.
-// KVB (with H): scales of the stage's block, as in SimtState; m2 and its f16
-// weights are per head.
-template <int D, int NT, bool H = false, bool KVB = false>
+template <int D, int NT, bool H = false>
 struct MmaState {
     static constexpr int KS = D / 16;  // k-steps of QK^T
     static constexpr int MT = D / 16;  // m-tiles of O^T
@@ -660,14 +563,12 @@ struct MmaState {
     float o[NT][MT][4];                // O^T accumulators
     float m[NT][2];                    // running max of heads nt*8 + 2*(lane%4) + {0,1}
     float l[NT][2];                    // this thread's share of the sums
-    float m2[NT][2];                   // KVB: references of the columns of o
-    float qup[NT][2];                  // KVB: the power of two that each head's q was divided by
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) { m[nt][c] = PKV_NEG_INF; m2[nt][c] = PKV_NEG_INF; l[nt][c] = 0.f; }
+            for (int c = 0; c < 2; ++c) { m[nt][c] = PKV_NEG_INF; l[nt][c] = 0.f; }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -691,34 +592,13 @@ struct MmaState {
                 if (head < g) {
                     b0 = *reinterpret_cast<const uint32_t *>(qs + head * D + col0);
                     b1 = *reinterpret_cast<const uint32_t *>(qs + head * D + col1);
-                    if constexpr (H && !KVB) {
+                    if constexpr (H) {
                         b0 = f16x2_from_f32(bf16lo_to_f32(b0), bf16hi_to_f32(b0));
                         b1 = f16x2_from_f32(bf16lo_to_f32(b1), bf16hi_to_f32(b1));
                     }
                 }
                 qb[nt][kk][0] = b0;
                 qb[nt][kk][1] = b1;
-            }
-            if constexpr (KVB) {
-                float amax = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(qb[nt][kk][c])), fabsf(bf16hi_to_f32(qb[nt][kk][c]))));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                float down, up;
-                unit_power(amax, down, up);
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        qb[nt][kk][c] = f16x2_from_f32(bf16lo_to_f32(qb[nt][kk][c]) * down,
-                                                       bf16hi_to_f32(qb[nt][kk][c]) * down);
-                // this lane's columns of S^T are heads 2 (lane % 4) + c
-#pragma unroll
-                for (int c = 0; c < 2; ++c) qup[nt][c] = __shfl_sync(0xffffffffu, up, (2 * (lane & 3) + c) * 4);
             }
         }
     }
@@ -727,8 +607,7 @@ struct MmaState {
     // stage); only then are scores past `valid` masked and the V operand's
     // rows of those tokens zeroed, so a full stage spends no instructions on it.
     template <bool PARTIAL>
-    __device__ __forceinline__ void stage(uint32_t ktile, uint32_t vtile, int valid, int lane, float scale_log2,
-                                          float vs = 1.f) {
+    __device__ __forceinline__ void stage(uint32_t ktile, uint32_t vtile, int valid, int lane, float scale_log2) {
         // S^T[token][head] = K . Q^T
         // two independent accumulator chains (even / odd k-steps), summed after
         float s[NT][4], s2[NT][4];
@@ -747,7 +626,7 @@ struct MmaState {
                 // (rows perm16(8-15), same), then the same for k-step kk + 1; lane l
                 // receives codes 4(l%4) .. +3 of its rows, as one 32-bit load each would
                 if ((kk & 1) == 0)
-                    ldmatrix_x4(tile_addr8<D>(ktile, perm16(ri + 8 * (mi & 1)), kk * 16 + 16 * (mi >> 1)), kw[0], kw[1],
+                    ldmatrix_x4(tile_addr8(ktile, perm16(ri + 8 * (mi & 1)), kk * 16 + 16 * (mi >> 1)), kw[0], kw[1],
                                 kw[2], kw[3]);
                 const uint32_t w0 = kw[2 * (kk & 1)], w1 = kw[2 * (kk & 1) + 1];
                 f16x2_from_e4m3x4(w0, a0, a2);
@@ -772,17 +651,14 @@ struct MmaState {
         const bool ok0 = !PARTIAL || (H ? perm16(t0) : t0) < valid;
         const bool ok1 = !PARTIAL || (H ? perm16(t0 + 8) : t0 + 8) < valid;
         uint32_t pb[NT][2];
-        const float lv = KVB ? scale_exponent(vs) : 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float alpha[2], p[4], z[4];
-            float my[2];  // KVB: the stage's max score of each column
             bool raise = false;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float sc = KVB ? scale_log2 * qup[nt][c] : scale_log2;
-                z[c] = ok0 ? s[nt][c] * sc : PKV_NEG_INF;
-                z[c + 2] = ok1 ? s[nt][c + 2] * sc : PKV_NEG_INF;
+                z[c] = ok0 ? s[nt][c] * scale_log2 : PKV_NEG_INF;
+                z[c + 2] = ok1 ? s[nt][c + 2] * scale_log2 : PKV_NEG_INF;
                 float mx = fmaxf(z[c], z[c + 2]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -791,24 +667,13 @@ struct MmaState {
                 const bool up = mx > m[nt][c] + kRescaleSlack;
                 alpha[c] = up ? exp2f(m[nt][c] - mx) : 1.f;
                 if (up) m[nt][c] = mx;
-                raise |= up && !KVB;
-                my[c] = mx;
+                raise |= up;
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 p[c] = exp2f(z[c] - m[nt][c]);
                 p[c + 2] = exp2f(z[c + 2] - m[nt][c]);
                 l[nt][c] = l[nt][c] * alpha[c] + p[c] + p[c + 2];
-                if constexpr (KVB) {  // from here on: the references and weights of o
-                    const float y = my[c] + lv;
-                    const bool up = y > m2[nt][c] + kRescaleSlack;
-                    alpha[c] = up ? exp2f(m2[nt][c] - y) : 1.f;
-                    if (up) m2[nt][c] = y;
-                    raise |= up;
-                    const float f = exp2f(fminf(m[nt][c] + lv - m2[nt][c], 126.f));  // see SimtState
-                    p[c] *= f;
-                    p[c + 2] *= f;
-                }
             }
             // accumulator layout (token row, head pair) -> operand layout of P^T
             pb[nt][0] = movmatrix_trans(H ? f16x2_from_f32(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
@@ -838,7 +703,7 @@ struct MmaState {
             uint32_t a0, a1, a2, a3;
             if constexpr (H) {
                 uint32_t r0, r1;
-                ldmatrix_b8_trans(tile_addr8<D>(vtile, lane & 15, mt * 16), r0, r1);
+                ldmatrix_b8_trans(tile_addr8(vtile, lane & 15, mt * 16), r0, r1);
                 f16x2_from_e4m3x4(r0, a0, a2);  // d = l/4: tokens 4j, 4j+1 and 4j+2, 4j+3
                 f16x2_from_e4m3x4(r1, a1, a3);  // d = l/4 + 8
             } else {
@@ -871,14 +736,6 @@ struct MmaState {
                 lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
                 lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
                 const int head = nt * 8 + 2 * (lane & 3) + c;
-                if constexpr (KVB) {  // from reference m2 to m
-                    const float f = m2[nt][c] == PKV_NEG_INF ? 0.f : exp2f(m2[nt][c] - m[nt][c]);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        o[nt][mt][c] *= f;
-                        o[nt][mt][c + 2] *= f;
-                    }
-                }
                 if (head < g) {
                     if (lane < 4) { mM[w * GPn + head] = m[nt][c]; mL[w * GPn + head] = lsum; }
                     float *row = mO + (w * GPn + head) * stride;
@@ -901,11 +758,7 @@ struct MmaState {
 // and the registers must not cut that to three.
 constexpr int decode_min_ctas(int PATH, int GPAD, bool KV8) { return (KV8 && PATH == 1 && GPAD <= 8) ? 4 : 1; }
 
-// KVB: an FP8 pool with a scale for each (block, kv head).  A stage lies in one
-// block; the lane that issues its tiles fetches the block's two scales into
-// the slot with cp.async, whose arrival is the second one that the slot's full
-// barrier waits for, so the producer never waits for a scale.
-template <int D, int PATH, int GSIMT, int GPAD, int NS, bool KV8 = false, bool KVB = false>
+template <int D, int PATH, int GSIMT, int GPAD, int NS, bool KV8 = false>
 __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV8))
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const DecodeParams p) {
@@ -913,9 +766,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
     static_assert(PATH != 0 || GSIMT == 1, "the CUDA-core path serves one query head per kv head");
     constexpr int GP = PATH == 0 ? GSIMT : GPAD;
     constexpr int NT = (GPAD + 7) / 8;
-    static_assert(!KVB || KV8, "block scales belong to an FP8 pool");
-    using L = DecodeSmem<D, GP, NS, KV8, KVB>;
-    constexpr int kFullArrivals = KVB ? 2 : 1;
+    static_assert(!KV8 || D == 128, "FP8 stage tiles are 128-byte rows (head dim 128)");
+    using L = DecodeSmem<D, GP, NS, KV8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // 1024-B alignment: the 128-byte swizzle pattern repeats every 1 KB.
     // Everything below indexes the shared array itself, so accesses stay in
@@ -942,11 +794,10 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
     float *mO = reinterpret_cast<float *>(smem + L::oMergeO);
     float *mM = reinterpret_cast<float *>(smem + L::oMergeM);
     float *mL = reinterpret_cast<float *>(smem + L::oMergeL);
-    float2 *slot_scales = reinterpret_cast<float2 *>(smem + L::oScales);  // KVB
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) { mbar_init(&full[i], kFullArrivals); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < NS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&qfull[i], 1); mbar_init(&qempty[i], W); }
         mbar_init(mfull, W);
         mbar_init(mempty, W);
@@ -1079,26 +930,15 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
                         info[slot] = si;
                         if (valid > 0) {
                             const uint32_t kt = tiles + slot * L::kStage;
-                            if constexpr (KVB) {
-                                if (row < p.pool_rows) {
-                                    const int e = row / p.bs;  // block * Hkv + head
-                                    cp_async4(&slot_scales[slot].x, p.kb_scales + e);
-                                    cp_async4(&slot_scales[slot].y, p.vb_scales + e);
-                                    cp_async_mbar_arrive(&full[slot]);
-                                } else {
-                                    slot_scales[slot] = make_float2(1.f, 1.f);
-                                    mbar_arrive(&full[slot]);
-                                }
-                            }
                             mbar_arrive_expect_tx(&full[slot], (uint32_t)L::kStage);
 #pragma unroll
                             for (int hf = 0; hf < L::kBoxes; ++hf) {
-                                const int x = hf * (L::kBoxRow / L::kElem);  // box column in elements
+                                const int x = hf * (128 / L::kElem);  // box column in elements
                                 tma_load_2d_u32(kt + hf * L::kHalfTile, &tmap_k, &full[slot], x, row);
                                 tma_load_2d_u32(kt + L::kTile + hf * L::kHalfTile, &tmap_v, &full[slot], x, row);
                             }
                         } else {
-                            mbar_arrive_count(&full[slot], kFullArrivals);
+                            mbar_arrive(&full[slot]);
                         }
                     }
                 }
@@ -1120,7 +960,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
                 ok = wait_or_abort(&empty[slot], ((gc / NS) & 1) ^ 1, abort_flag);
                 if (ok) {
                     info[slot].ord = -1;
-                    mbar_arrive_count(&full[slot], kFullArrivals);
+                    mbar_arrive(&full[slot]);
                 }
                 ++gc;
             }
@@ -1143,8 +983,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
         uint32_t mc = 0;   // merges done (each completes one phase of mempty)
         uint32_t mfc = 0;  // merges of single partitions (each completes one phase of mfull)
         float scale_log2 = p.scale_log2;
-        SimtState<D, KV8, KVB> st0;
-        MmaState<D, (PATH == 1 ? NT : 1), KV8, KVB> st1;
+        SimtState<D, KV8> st0;
+        MmaState<D, (PATH == 1 ? NT : 1), KV8> st1;
         while (true) {
             const uint32_t slot = gc % NS;
             if (!wait_or_abort(&full[slot], (gc / NS) & 1, abort_flag)) break;
@@ -1157,7 +997,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
                 const __nv_bfloat16 *qs = qbuf + qb * (L::kQBuf / 2);
                 if constexpr (PATH == 0) {
                     st0.reset();
-                    st0.load_q(qs, lane, KV8 && !KVB ? scale_log2 * __ldg(p.k_scale + si.h) : scale_log2);
+                    st0.load_q(qs, lane, KV8 ? scale_log2 * __ldg(p.k_scale + si.h) : scale_log2);
                 } else {
                     st1.reset();
                     st1.load_q(qs, lane, p.g);
@@ -1168,17 +1008,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
             if (si.valid > 0) {
                 const uint32_t kt = tiles + slot * L::kStage;
                 const bool partial = si.valid < kStageTok;  // warp-uniform
-                if constexpr (KVB) {
-                    const float2 sc = slot_scales[slot];
-                    if constexpr (PATH == 0) {
-                        if (partial) st0.template stage<true>(kt, kt + L::kTile, si.valid, lane, sc.x, sc.y);
-                        else st0.template stage<false>(kt, kt + L::kTile, si.valid, lane, sc.x, sc.y);
-                    } else {
-                        const float sl = scale_log2 * sc.x;
-                        if (partial) st1.template stage<true>(kt, kt + L::kTile, si.valid, lane, sl, sc.y);
-                        else st1.template stage<false>(kt, kt + L::kTile, si.valid, lane, sl, sc.y);
-                    }
-                } else if constexpr (PATH == 0) {
+                if constexpr (PATH == 0) {
                     if (partial) st0.template stage<true>(kt, kt + L::kTile, si.valid, lane);
                     else st0.template stage<false>(kt, kt + L::kTile, si.valid, lane);
                 } else {
@@ -1216,7 +1046,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_min_ctas(PATH, GPAD, KV
                             Lsum = fmaf(mL[u * GP + j], f[u], Lsum);
                         }
                         float invL = Lsum > 0.f ? 1.f / Lsum : 0.f;
-                        if constexpr (KV8 && !KVB) invL *= __ldg(p.v_scale + si.h);
+                        if constexpr (KV8) invL *= __ldg(p.v_scale + si.h);
 #pragma unroll
                         for (int i = 0; i < D / 32; ++i) {
                             const int d = lane + 32 * i;

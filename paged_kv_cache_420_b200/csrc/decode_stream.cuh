@@ -1,0 +1,870 @@
+// decode_stream.cuh -- decode attention over a block-scaled 8-bit pool, and
+// over selected blocks (bf16 or block-scaled 8-bit), for sm_100a.
+//
+// All 16-token stages of all (sequence, kv head) units form one line,
+// sequence-major, and every consumer warp of the grid takes one contiguous
+// stretch of it, all of the same length to a stage: no plan kernel, no work
+// counter, no partition size, and nothing is left for a tail however the
+// lengths are spread, from one long sequence to thousands of short ones.  A
+// warp runs through the units of its stretch with one softmax state.  A unit
+// that lies within a stretch is written out by its warp; the parts of a unit
+// that stretches cut are merged in two steps, within the CTA (whose four
+// stretches are neighbours), then, where a unit goes on over CTAs, through at
+// most two records of each CTA that a second kernel merges.
+//
+//   dense:    unit (s, h) has ceil(context / 16) stages; each CTA adds up the
+//             contexts itself (they are few, and in L2)
+//   selected: unit (s, h) has K entries of block_size / 16 stages each
+//
+// In a CTA one producer warp feeds four rings, one for each consumer warp: 8
+// of its lanes look up the next 8 stages of each stretch (table entries, and
+// the selection before them) a group ahead, and issue their TMA loads, the
+// scales of the stage's block (cp.async) and, where a unit begins, a prefetch
+// of its q.
+#pragma once
+
+#include "decode.cuh"
+
+namespace pkv {
+
+// ------------------------------------------------------------- arithmetic ----
+
+// The power of two that brings a largest magnitude into [1, 2) (1/2 .. 4 at
+// the ends of the range): q is converted to f16 with it, so its elements keep
+// 11 bits down to 2^-14 of the head's largest whatever their size.  The
+// inverse, for the scores, is exact too.
+__device__ __forceinline__ void unit_power(float amax, float &down, float &up) {
+    const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
+    down = __uint_as_float((uint32_t)(254 - e) << 23);
+    up = __uint_as_float((uint32_t)e << 23);
+}
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x; results below 2^-126 are 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Byte address of e4m3 element (row r, column c) of a stage tile: one 128-byte
+// line per row at head dim 128, 16-byte chunks XOR-swizzled with (r & 7); two
+// 64-byte rows per line at 64, chunks XOR-swizzled with the line's number.
+template <int D>
+__device__ __forceinline__ uint32_t tile_addr_e4m3(uint32_t tile, int r, int c) {
+    if constexpr (D == 64) return tile + r * 64 + ((((c >> 4) ^ ((r >> 1) & 3))) << 4) + (c & 15);
+    return tile_addr8(tile, r, c);
+}
+
+// The attention of one warp over stages of 16 tokens, for the g <= 8 NT query
+// heads of a kv head, on the tensor cores (a single head as well: the products
+// of the unused columns are free, and the CUDA-core form takes twice the
+// instructions):
+//   S^T[16 tokens][8 heads] = K Q^T,  O^T[D][8 heads] += V^T P^T
+// in the fragment layouts of MmaState.  Its instructions bound it, not the
+// tensor cores: a warp issues one every four cycles, so what is done for each
+// stage beside the products and conversions is kept small.
+//
+// bf16 pool: the weights enter the second product as a sum of two bf16 (17
+// bits): twice the products, which are free.
+//
+// e4m3 pool, scales ks and vs of the stage's block: the codes are exact as
+// f16, and a stage's tokens are taken in perm16 order.  ks multiplies the
+// summed scores.  vs is a part of a token's weight, 2^(z - m) vs, and blocks
+// may differ in it by any power of two, while the weight is used as f16: so O
+// has references of its own, m2 ~ max(z + log2 vs), and holds
+// sum 2^(z + log2 vs - m2) code, beside m and l of the softmax.
+//
+// Both references are raised only when a value exceeds them by kRescaleSlack
+// (weights stay below 2^8), so a stage compares its values with one threshold
+// for each head and votes; the maxima are worked out only in the stages that
+// raise one.
+template <int D, int NT, bool KV8>
+struct TileState {
+    static constexpr int KS = D / 16;  // k-steps of K Q^T
+    static constexpr int MT = D / 16;  // m-tiles of O^T
+    static constexpr int KL = KV8 ? KS / 2 : KS;  // matrix loads of a K tile
+    uint32_t qb[NT][KS][2];  // B fragments of Q^T
+    float o[NT][MT][4];      // O^T accumulators
+    float m[NT][2];          // reference of the scores of heads nt*8 + 2*(lane%4) + {0,1}
+    float m2[NT][2];         // e4m3: of the columns of O^T
+    float l[NT][2];          // this thread's share of the sums
+    float sc[NT][2];         // e4m3: scale * log2 e times the power of two that a head's q was divided by
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) { m[nt][c] = PKV_NEG_INF; m2[nt][c] = PKV_NEG_INF; l[nt][c] = 0.f; }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[nt][mt][c] = 0.f;
+        }
+    }
+
+    // B fragment of Q^T (k = head dim, n = head); heads >= g are zero.  e4m3:
+    // k slots 2j, 2j+1, 2j+8, 2j+9 hold columns 4j .. 4j+3.
+    __device__ __forceinline__ void load_q(const __nv_bfloat16 *q, int lane, int g, float scale_log2) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int head = nt * 8 + (lane >> 2);
+            const __nv_bfloat16 *row = q + head * D + (KV8 ? 4 : 2) * (lane & 3);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                qb[nt][kk][0] = qb[nt][kk][1] = 0u;
+                if (head < g) {
+                    if constexpr (KV8) {
+                        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(row + kk * 16));
+                        qb[nt][kk][0] = x.x;
+                        qb[nt][kk][1] = x.y;
+                    } else {
+                        qb[nt][kk][0] = __ldg(reinterpret_cast<const uint32_t *>(row + kk * 16));
+                        qb[nt][kk][1] = __ldg(reinterpret_cast<const uint32_t *>(row + kk * 16 + 8));
+                    }
+                }
+            }
+            if constexpr (KV8) {
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(qb[nt][kk][c])), fabsf(bf16hi_to_f32(qb[nt][kk][c]))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                float down, up;
+                unit_power(amax, down, up);
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        qb[nt][kk][c] = f16x2_from_f32(bf16lo_to_f32(qb[nt][kk][c]) * down,
+                                                       bf16hi_to_f32(qb[nt][kk][c]) * down);
+                // this lane's columns of S^T are heads 2 (lane % 4) + c
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    sc[nt][c] = scale_log2 * __shfl_sync(0xffffffffu, up, (2 * (lane & 3) + c) * 4);
+            }
+        }
+    }
+
+    // Raises the references that a stage's values exceed (all lanes).
+    __device__ __forceinline__ void raise(const float (&z)[NT][4], float lv) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float mx = fmaxf(z[nt][c], z[nt][c + 2]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                float fo = 1.f;
+                if (mx > m[nt][c] + kRescaleSlack) {
+                    const float f = ex2(m[nt][c] - mx);
+                    m[nt][c] = mx;
+                    l[nt][c] *= f;
+                    if constexpr (!KV8) fo = f;
+                }
+                if constexpr (KV8) {
+                    const float y = mx + lv;
+                    if (y > m2[nt][c] + kRescaleSlack) {
+                        fo = ex2(m2[nt][c] - y);
+                        m2[nt][c] = y;
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[nt][mt][c] *= fo;
+                    o[nt][mt][c + 2] *= fo;
+                }
+            }
+        }
+    }
+
+    // PARTIAL: fewer than 16 valid tokens; only then are scores past `valid`
+    // masked and the V operand's rows of those tokens zeroed.  scale: scale *
+    // log2 e (bf16).  The tiles are 1 KB-aligned, so a lane's addresses in
+    // them differ by an exclusive or.
+    template <bool PARTIAL>
+    __device__ __forceinline__ void stage(uint32_t ktile, uint32_t vtile, int valid, int lane, float scale, float ks,
+                                          float vs) {
+        const int mi = lane >> 3, ri = lane & 7;
+        uint32_t ka[KL][4], va[MT][KV8 ? 2 : 4];
+        {
+            const uint32_t at = KV8 ? tile_addr_e4m3<D>(ktile, perm16(ri + 8 * (mi & 1)), 16 * (mi >> 1))
+                                    : tile_addr(ktile, ri + 8 * (mi & 1), 8 * (mi >> 1));
+#pragma unroll
+            for (int i = 0; i < KL; ++i)
+                ldmatrix_x4(KV8 ? at ^ (32 * i) : (at ^ (32 * (i & 3))) + (i >> 2) * (kStageTok * 128), ka[i][0], ka[i][1],
+                            ka[i][2], ka[i][3]);
+        }
+        // two chains of products (even / odd k-steps), added after
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) { s[nt][c] = 0.f; s2[nt][c] = 0.f; }
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (KV8) {
+                f16x2_from_e4m3x4(ka[kk / 2][2 * (kk & 1)], a0, a2);
+                f16x2_from_e4m3x4(ka[kk / 2][2 * (kk & 1) + 1], a1, a3);
+            } else {
+                a0 = ka[kk][0]; a1 = ka[kk][1]; a2 = ka[kk][2]; a3 = ka[kk][3];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float(&acc)[4] = (kk & 1) ? s2[nt] : s[nt];
+                if constexpr (KV8) mma_f16_16816(acc[0], acc[1], acc[2], acc[3], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
+                else mma_bf16_16816(acc[0], acc[1], acc[2], acc[3], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
+            }
+        }
+        // the V operands are on their way while the weights are worked out
+        {
+            const uint32_t at = KV8 ? tile_addr_e4m3<D>(vtile, lane & 15, 0)
+                                    : tile_addr(vtile, ri + 8 * (mi >> 1), 8 * (mi & 1));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (KV8) ldmatrix_b8_trans(at ^ (16 * mt), va[mt][0], va[mt][1]);
+                else ldmatrix_x4_trans((at ^ (32 * (mt & 3))) + (mt >> 2) * (kStageTok * 128), va[mt][0], va[mt][1], va[mt][2],
+                                       va[mt][3]);
+            }
+        }
+        const int t0 = lane >> 2;  // rows t0 and t0 + 8 of S^T
+        const bool ok0 = !PARTIAL || (KV8 ? perm16(t0) : t0) < valid;
+        const bool ok1 = !PARTIAL || (KV8 ? perm16(t0 + 8) : t0 + 8) < valid;
+        float lv = 0.f;
+        if constexpr (KV8) lv = vs > 0.f ? __log2f(vs) : -1000.f;  // a scale that is not above zero holds no value
+        float z[NT][4];
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float f = KV8 ? sc[nt][c] * ks : scale;
+                z[nt][c] = ok0 ? (s[nt][c] + s2[nt][c]) * f : PKV_NEG_INF;
+                z[nt][c + 2] = ok1 ? (s[nt][c + 2] + s2[nt][c + 2]) * f : PKV_NEG_INF;
+                const float top = (KV8 ? fminf(m[nt][c], m2[nt][c] - lv) : m[nt][c]) + kRescaleSlack;
+                over |= fmaxf(z[nt][c], z[nt][c + 2]) > top;
+            }
+        if (__any_sync(0xffffffffu, over)) raise(z, lv);
+        uint32_t pb[NT][2], pc[KV8 ? 1 : NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float p[4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                p[c] = ex2(z[nt][c] - m[nt][c]);
+                p[c + 2] = ex2(z[nt][c + 2] - m[nt][c]);
+                l[nt][c] += p[c] + p[c + 2];
+                if constexpr (KV8) {
+                    p[c] = ex2(z[nt][c] + (lv - m2[nt][c]));
+                    p[c + 2] = ex2(z[nt][c + 2] + (lv - m2[nt][c]));
+                }
+            }
+            // accumulator layout (token row, head pair) -> operand layout of P^T
+            if constexpr (KV8) {
+                pb[nt][0] = movmatrix_trans(f16x2_from_f32(p[0], p[1]));
+                pb[nt][1] = movmatrix_trans(f16x2_from_f32(p[2], p[3]));
+            } else {
+                const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
+                pb[nt][0] = movmatrix_trans(h0);
+                pb[nt][1] = movmatrix_trans(h1);
+                pc[nt][0] = movmatrix_trans(pack_bf16x2(p[0] - bf16lo_to_f32(h0), p[1] - bf16hi_to_f32(h0)));
+                pc[nt][1] = movmatrix_trans(pack_bf16x2(p[2] - bf16lo_to_f32(h1), p[3] - bf16hi_to_f32(h1)));
+            }
+        }
+        // token masks of this thread's V^T operand halves
+        uint32_t mask01 = 0xffffffffu, mask23 = 0xffffffffu;
+        if constexpr (PARTIAL) {
+            const int j0 = KV8 ? 4 * (lane & 3) : 2 * (lane & 3);
+            const int j2 = KV8 ? j0 + 2 : j0 + 8;
+            mask01 = (j0 < valid ? 0x0000ffffu : 0u) | (j0 + 1 < valid ? 0xffff0000u : 0u);
+            mask23 = (j2 < valid ? 0x0000ffffu : 0u) | (j2 + 1 < valid ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (KV8) {
+                f16x2_from_e4m3x4(va[mt][0], a0, a2);  // d = l/4: tokens 4j, 4j+1 and 4j+2, 4j+3
+                f16x2_from_e4m3x4(va[mt][1], a1, a3);  // d = l/4 + 8
+            } else {
+                a0 = va[mt][0]; a1 = va[mt][1]; a2 = va[mt][2]; a3 = va[mt][3];
+            }
+            if constexpr (PARTIAL) { a0 &= mask01; a1 &= mask01; a2 &= mask23; a3 &= mask23; }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float(&acc)[4] = o[nt][mt];
+                if constexpr (KV8) {
+                    mma_f16_16816(acc[0], acc[1], acc[2], acc[3], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                } else {
+                    mma_bf16_16816(acc[0], acc[1], acc[2], acc[3], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    mma_bf16_16816(acc[0], acc[1], acc[2], acc[3], a0, a1, a2, a3, pc[nt][0], pc[nt][1]);
+                }
+            }
+        }
+    }
+
+    // l summed over its lanes, and what brings a column of O^T to reference m.
+    __device__ __forceinline__ void finish(int nt, int c, float &lsum, float &f) {
+        lsum = l[nt][c];
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+        f = !KV8 ? 1.f : m2[nt][c] == PKV_NEG_INF ? 0.f : ex2(m2[nt][c] - m[nt][c]);
+    }
+
+    // This warp's part (m, l, O) of a unit: rows of `stride` floats.
+    __device__ __forceinline__ void store_part(float *acc, int stride, float *pm, float *pl, int lane, int g) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float lsum, f;
+                finish(nt, c, lsum, f);
+                const int head = nt * 8 + 2 * (lane & 3) + c;
+                if (head >= g) continue;
+                if (lane < 4) { pm[head] = m[nt][c]; pl[head] = lsum; }
+                float *row = acc + head * stride + (lane >> 2);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    row[mt * 16] = o[nt][mt][c] * f;
+                    row[mt * 16 + 8] = o[nt][mt][c + 2] * f;
+                }
+            }
+    }
+
+    // The normalised rows of a unit that this warp took alone.
+    __device__ __forceinline__ void write_out(__nv_bfloat16 *out, int lane, int g) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float lsum;
+                finish(nt, c, lsum, f[c]);
+                f[c] = lsum > 0.f || lsum != lsum ? __fdividef(f[c], lsum) : 0.f;
+            }
+            const int head = nt * 8 + (lane >> 2);  // after the transpose
+            uint32_t *row = reinterpret_cast<uint32_t *>(out + head * D + 2 * (lane & 3));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t x = movmatrix_trans(pack_bf16x2(o[nt][mt][0] * f[0], o[nt][mt][1] * f[1]));
+                const uint32_t y = movmatrix_trans(pack_bf16x2(o[nt][mt][2] * f[0], o[nt][mt][3] * f[1]));
+                if (head < g) {
+                    row[mt * 8] = x;
+                    row[mt * 8 + 4] = y;
+                }
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------- work ----
+
+constexpr int kStreamGroup = 8;  // stages that a stretch's lanes look up at once
+static_assert(kConsumerWarps * kStreamGroup == 32, "a lane of the producer for each stage of a group");
+
+struct StreamParams {
+    const __nv_bfloat16 *q;       // [B][Hq][D]
+    __nv_bfloat16 *out;           // [B][Hq][D]
+    const int32_t *block_tables;  // [B][MBS]
+    const int32_t *context_lens;  // [B]
+    const int32_t *selected;      // [B][Hkv][K] (selected blocks only)
+    const float *k_scales;        // [NB][Hkv] (e4m3 pool)
+    const float *v_scales;
+    float *cut;                   // workspace: [CTAs][W][g][D], the parts at the beginnings of warps' stretches
+    int4 *meta;                   // workspace: [CTAs] (unit of record 0 or -1, whether the unit ends there, unit of record 1 or -1)
+    float2 *rec_ml;               // workspace: [CTAs][2][g] = (m, l)
+    float *rec_acc;               // workspace: [CTAs][2][g][D]
+    int B, Hq, Hkv, g, MBS, bs, NB, K, max_ctx;
+    int pool_rows;
+    int min_stages;  // of a stretch, while there are fewer stages than fill the grid
+    float scale_log2;
+};
+
+// A part of a unit that a warp leaves behind: the unit, and whether the unit
+// begins and ends in it.
+struct StreamPart {
+    short begins, ends;
+    int unit;
+};
+
+// What a consumer has to know of a stage.
+struct __align__(16) StreamStage {
+    int unit;
+    int valid;  // tokens; 0: none (nothing was loaded)
+    int first;  // the first of its unit in this stretch: fresh state, q in the slot
+    int last;   // the last: 0 no, 1 the unit is complete, 2 its beginning was cut off (3: and it ends here), 4 its end is cut off
+};
+
+template <int D, int GP, int NS, bool KV8>
+struct StreamSmem {
+    static constexpr int kW = kConsumerWarps;
+    static constexpr int kElem = KV8 ? 1 : 2;                           // bytes per K/V element
+    static constexpr int kBoxRow = D * kElem < 128 ? D * kElem : 128;   // bytes of a TMA box's row
+    static constexpr int kBox = kStageTok * kBoxRow;
+    static constexpr int kBoxes = D * kElem / kBoxRow;
+    static constexpr int kTile = kStageTok * D * kElem;                 // a K (or V) tile
+    static constexpr int kStage = 2 * kTile;
+    static constexpr int kStride = D + 4;                               // floats of a part's row, padded against bank conflicts
+    static constexpr int kPart = GP * kStride * 4;
+    static constexpr int oTiles = 0;                                    // the rings; the parts at the stretches' ends reuse them
+    static constexpr int oM = oTiles + NS * kStage;                     // [2 W][GP]: of the parts at the beginnings, then the ends
+    static constexpr int oL = oM + 2 * kW * GP * 4;
+    static constexpr int oFactor = oL + 2 * kW * GP * 4;
+    static constexpr int oPartInfo = oFactor + 2 * kW * GP * 4;         // StreamPart [2 W]
+    static constexpr int oBars = (oPartInfo + 2 * kW * 8 + 7) / 8 * 8;
+    static constexpr int oScales = oBars + 2 * NS * 8;
+    static constexpr int oInfo = (oScales + (KV8 ? NS * 8 : 0) + 15) / 16 * 16;
+    static constexpr int oScan = oInfo + NS * 16;                       // long long [threads]
+    static constexpr int oWarpSum = oScan + kDecodeThreads * 8;
+    static constexpr int oAbort = oWarpSum + 8 * 8;
+    static constexpr int kBytes = oAbort + 16;
+    static_assert(kW * kPart <= NS * kStage, "the parts at the stretches' ends fit into the rings");
+};
+
+// CTAs of an SM that the registers must allow.
+constexpr int stream_min_ctas(int GPAD, bool KV8) { return GPAD > 8 ? 2 : KV8 ? 4 : 3; }
+
+// Where a CTA's and a warp's stretch begins: `total` stages over `parts`.
+__device__ __forceinline__ long long stretch_begin(long long total, int parts, int i) {
+    return (total / parts) * i + (total % parts) * i / parts;
+}
+
+template <int D, int GPAD, int NS, bool KV8, bool SEL>
+__global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
+    stream_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                         const StreamParams p) {
+    constexpr int W = kConsumerWarps;
+    constexpr int GP = GPAD;
+    constexpr int NT = (GPAD + 7) / 8;
+    constexpr int DEPTH = NS / W;  // slots of a ring
+    constexpr int kFullArrivals = KV8 ? 2 : 1;
+    using L = StreamSmem<D, GP, NS, KV8>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::oBars);
+    uint64_t *empty = full + NS;
+    float2 *slot_scales = reinterpret_cast<float2 *>(smem + L::oScales);
+    StreamStage *info = reinterpret_cast<StreamStage *>(smem + L::oInfo);
+    StreamPart *part_info = reinterpret_cast<StreamPart *>(smem + L::oPartInfo);
+    float *mM = reinterpret_cast<float *>(smem + L::oM);
+    float *mL = reinterpret_cast<float *>(smem + L::oL);
+    long long *scan = reinterpret_cast<long long *>(smem + L::oScan);
+    long long *warp_sum = reinterpret_cast<long long *>(smem + L::oWarpSum);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::oAbort);
+    const uint32_t tiles = smem_u32(smem + L::oTiles);
+    float *factor = reinterpret_cast<float *>(smem + L::oFactor);
+    // Part i of the CTA: 0 .. W - 1 at a stretch's beginning, which is put into
+    // the workspace while the warp goes on, W .. 2 W - 1 at its end.
+    float *cut = p.cut + (size_t)blockIdx.x * W * p.g * D;
+    float *ends = reinterpret_cast<float *>(smem + L::oTiles);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) { mbar_init(&full[i], kFullArrivals); mbar_init(&empty[i], 1); }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        if ((smem_u32(smem_raw) & 1023u) != 0) {  // the swizzle pattern repeats every 1 KB
+            raise_error(PKV_DEVERR_LAYOUT);
+            *abort_flag = 1;
+        }
+    }
+    if (tid < 2 * W) part_info[tid].unit = -1;
+    grid_dependency_wait();
+
+    const long long ctx_cap = min((long long)p.MBS * p.bs, (long long)p.max_ctx);
+    auto context = [&](int s, bool report) -> int {
+        const int n = __ldg(p.context_lens + s);
+        if (n < 0 || n > ctx_cap) {
+            if (report) raise_error(PKV_DEVERR_CONTEXT);
+            return n < 0 ? 0 : (int)ctx_cap;
+        }
+        return n;
+    };
+    const int spe = p.bs / kStageTok;  // stages of a block
+    const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;  // sequences whose stages a thread adds up
+    long long total;
+    if constexpr (SEL) {
+        total = (long long)p.B * p.Hkv * p.K * spe;
+        if (blockIdx.x == 0)
+            for (int s = tid; s < p.B; s += kDecodeThreads) context(s, true);
+    } else {
+        long long sum = 0;
+        for (int s = tid * per; s < min(p.B, (tid + 1) * per); ++s)
+            sum += (context(s, blockIdx.x == 0) + kStageTok - 1) / kStageTok;
+        sum *= p.Hkv;
+        long long incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+        for (int w = 0; w <= W; ++w) {
+            before += w < warp ? warp_sum[w] : 0;
+            total += warp_sum[w];
+        }
+        scan[tid] = before + incl - sum;  // the stages before this thread's sequences
+        // empty sequences get a zero row
+        const int vec = p.Hq * D / 8;
+        for (int s = blockIdx.x; s < p.B; s += gridDim.x)
+            if (context(s, false) == 0)
+                for (int i = tid; i < vec; i += kDecodeThreads)
+                    reinterpret_cast<uint4 *>(p.out)[(size_t)s * vec + i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, total / (W * p.min_stages)));
+    if ((int)blockIdx.x >= ctas || total == 0) {
+        if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, -1, 0);
+        return;
+    }
+    const long long A = stretch_begin(total, ctas, blockIdx.x), E = stretch_begin(total, ctas, blockIdx.x + 1);
+    auto warp_begin = [&](int w) { return A + (E - A) * w / W; };
+
+    if (warp == W) {
+        // ------------------------------------------------------ producer --
+        const int j = lane / kStreamGroup, sub = lane % kStreamGroup;
+        const long long a = warp_begin(j), b = warp_begin(j + 1);
+        const int len = (int)(b - a);
+        int longest = len;
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, 8));
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, 16));
+        // dense: this lane's sequence and the line's stages before it
+        int cs = 0, nst = 0, n = 0;
+        long long base = 0;
+        if constexpr (!SEL) {
+            int lo = 0, hi = kDecodeThreads - 1;  // the last thread whose sequences begin at or before a
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (scan[mid] <= a) lo = mid; else hi = mid - 1;
+            }
+            cs = min(lo * per, p.B - 1);
+            base = scan[lo];
+            n = context(cs, false);
+            nst = (n + kStageTok - 1) / kStageTok;
+        }
+        struct Stage {
+            StreamStage st;
+            int row;
+        };
+        // stage k of this lane's stretch
+        auto look_up = [&](int k) -> Stage {
+            Stage r;
+            r.row = p.pool_rows;
+            r.st.unit = 0; r.st.valid = 0; r.st.first = 0; r.st.last = 0;
+            if (k >= len) return r;
+            const long long x = a + k;
+            int s, h, i, len_u;  // stage i of len_u of unit (s, h)
+            if constexpr (SEL) {
+                len_u = p.K * spe;
+                const long long unit = x / len_u;
+                i = (int)(x - unit * len_u);
+                s = (int)(unit / p.Hkv);
+                h = (int)(unit - (long long)s * p.Hkv);
+            } else {
+                while (x >= base + (long long)nst * p.Hkv) {
+                    base += (long long)nst * p.Hkv;
+                    n = context(++cs, false);
+                    nst = (n + kStageTok - 1) / kStageTok;
+                }
+                s = cs;
+                len_u = nst;
+                const long long off = x - base;
+                h = (int)(off / nst);
+                i = (int)(off - (long long)h * nst);
+            }
+            r.st.unit = s * p.Hkv + h;
+            const bool begins = x - i >= a, ends = x - i + len_u <= b;
+            r.st.first = i == 0 || k == 0;
+            if (r.st.first)  // its q, for the consumer's loads
+                for (int y = 0; y < p.g * D * 2; y += 128)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(p.q) + (size_t)r.st.unit * p.g * D * 2 + y));
+            r.st.last = i == len_u - 1 || k == len - 1 ? (begins ? (ends ? 1 : 4) : (ends ? 3 : 2)) : 0;
+            int blk = i / spe, off_blk = (i - blk * spe) * kStageTok;  // logical block, token in it
+            if constexpr (SEL) {
+                n = context(s, false);
+                const int e = blk;
+                blk = __ldg(p.selected + (size_t)r.st.unit * p.K + e);
+                if (blk < 0) return r;
+                if (blk >= (n + p.bs - 1) / p.bs) {  // behind the context
+                    raise_error(PKV_DEVERR_BLOCK);
+                    return r;
+                }
+            }
+            r.st.valid = min(kStageTok, n - blk * p.bs - off_blk);
+            if (r.st.valid <= 0) {
+                r.st.valid = 0;
+                return r;
+            }
+            const int id = __ldg(p.block_tables + (size_t)s * p.MBS + blk);
+            if (id < 0 || id >= p.NB) raise_error(PKV_DEVERR_BLOCK);  // reads the zero fill
+            else r.row = (id * p.Hkv + h) * p.bs + off_blk;
+            return r;
+        };
+        bool ok = true;
+        int issued = 0;
+        Stage next = look_up(sub);
+        for (int k0 = 0; k0 < longest && ok; k0 += kStreamGroup) {
+            const Stage cur = next;
+            next = look_up(k0 + kStreamGroup + sub);
+            for (int t = 0; t < kStreamGroup && ok; ++t) {
+                const int k = k0 + t;
+                bool lane_ok = true;
+                if (sub == t && k < len) {
+                    const int slot = j * DEPTH + k % DEPTH;
+                    lane_ok = wait_slot(&empty[slot], ((k / DEPTH) & 1) ^ 1, abort_flag);
+                    if (lane_ok) {
+                        info[slot] = cur.st;
+                        const bool load = cur.st.valid > 0;
+                        if constexpr (KV8) {
+                            if (load && cur.row < p.pool_rows) {
+                                const int e = cur.row / p.bs;  // block * Hkv + head
+                                cp_async4(&slot_scales[slot].x, p.k_scales + e);
+                                cp_async4(&slot_scales[slot].y, p.v_scales + e);
+                                cp_async_mbar_arrive(&full[slot]);
+                            } else {
+                                slot_scales[slot] = make_float2(1.f, 1.f);
+                                mbar_arrive(&full[slot]);
+                            }
+                        }
+                        mbar_arrive_expect_tx(&full[slot], load ? (uint32_t)L::kStage : 0u);
+                        if (load) {
+                            const uint32_t kt = tiles + slot * L::kStage;
+#pragma unroll
+                            for (int hf = 0; hf < L::kBoxes; ++hf) {
+                                const int x = hf * (L::kBoxRow / L::kElem);
+                                tma_load_2d_u32(kt + hf * L::kBox, &tmap_k, &full[slot], x, cur.row);
+                                tma_load_2d_u32(kt + L::kTile + hf * L::kBox, &tmap_v, &full[slot], x, cur.row);
+                            }
+                        }
+                        issued = k + 1;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, lane_ok);
+            }
+        }
+        // After a wait that gave up, what this lane has in flight still has to land.
+        if (!ok)
+            for (int k = max(0, issued - kStreamGroup); k < issued; ++k)
+                if (k % kStreamGroup == sub) mbar_wait_bounded(&full[j * DEPTH + k % DEPTH], (k / DEPTH) & 1, kWaitLimitNs);
+    } else {
+        // ------------------------------------------------------ consumer --
+        const int len = (int)(warp_begin(warp + 1) - warp_begin(warp));
+        TileState<D, NT, KV8> state;
+        auto store_part = [&](int i, float *acc, int stride, const StreamStage &st) {
+            state.store_part(acc, stride, mM + i * GP, mL + i * GP, lane, p.g);
+            if (lane == 0) { part_info[i].unit = st.unit; part_info[i].begins = st.last == 4; part_info[i].ends = st.last == 3; }
+        };
+        StreamStage tail;
+        tail.unit = -1; tail.last = 0;
+        for (int k = 0; k < len; ++k) {
+            const int slot = warp * DEPTH + k % DEPTH;
+            if (!wait_or_abort(&full[slot], (k / DEPTH) & 1, abort_flag)) break;
+            const StreamStage st = info[slot];
+            if (st.first) {
+                state.reset();
+                state.load_q(p.q + (size_t)st.unit * p.g * D, lane, p.g, p.scale_log2);
+            }
+            if (st.valid > 0) {
+                const uint32_t kt = tiles + slot * L::kStage;
+                const bool partial = st.valid < kStageTok;
+                float ks = 1.f, vs = 1.f;
+                if constexpr (KV8) {
+                    const float2 sc = slot_scales[slot];
+                    ks = sc.x;
+                    vs = sc.y;
+                }
+                if (partial) state.template stage<true>(kt, kt + L::kTile, st.valid, lane, p.scale_log2, ks, vs);
+                else state.template stage<false>(kt, kt + L::kTile, st.valid, lane, p.scale_log2, ks, vs);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (st.last == 1) {
+                state.write_out(p.out + (size_t)st.unit * p.g * D, lane, p.g);
+            } else if (st.last == 4 || (st.last != 0 && k == len - 1)) {
+                tail = st;  // the stretch ends with it: it stays in registers
+            } else if (st.last != 0) {
+                store_part(warp, cut + (size_t)warp * p.g * D, D, st);
+            }
+        }
+        named_barrier_sync(1, kDecodeThreads);  // every ring has run dry
+        if (tail.unit >= 0) store_part(W + warp, ends + warp * (L::kPart / 4), L::kStride, tail);
+    }
+    if (warp == W) named_barrier_sync(1, kDecodeThreads);
+    __syncthreads();
+    grid_launch_dependents();
+
+    // The parts in the line's order: warp 0's first, warp 0's last, warp 1's
+    // first, ...  Neighbours of one unit belong together.  Thread (x, head)
+    // works out part x's factor, and its group's sums if it is the first.
+    auto part_at = [&](int x) { return (x >> 1) + (x & 1) * W; };
+    auto unit_at = [&](int x) { return part_info[part_at(x)].unit; };
+    for (int i = tid; i < 2 * W * p.g; i += kDecodeThreads) {
+        const int x = i / p.g, hd = i - x * p.g, unit = unit_at(x);
+        if (unit < 0) continue;
+        float M = PKV_NEG_INF;
+#pragma unroll
+        for (int y = 0; y < 2 * W; ++y)
+            if (unit_at(y) == unit) M = fmaxf(M, mM[part_at(y) * GP + hd]);
+        const float mu = mM[part_at(x) * GP + hd];
+        factor[x * GP + hd] = mu == PKV_NEG_INF ? 0.f : ex2(mu - M);
+    }
+    __syncthreads();
+    int4 meta = make_int4(-1, 0, -1, 0);
+    for (int x = 0; x < 2 * W;) {
+        const int unit = unit_at(x);
+        if (unit < 0) { ++x; continue; }
+        int y = x + 1, last = x;  // parts x .. last (others than `unit` among them: none)
+        for (; y < 2 * W && (unit_at(y) < 0 || unit_at(y) == unit); ++y)
+            if (unit_at(y) == unit) last = y;
+        // a group that does not begin with its unit goes back before the CTA
+        const bool begins = part_info[part_at(x)].begins != 0, done = part_info[part_at(last)].ends != 0;
+        float *rec = p.rec_acc + ((size_t)blockIdx.x * 2 + begins) * p.g * D;
+        for (int i = tid; i < p.g * D / 4; i += kDecodeThreads) {
+            const int hd = i / (D / 4), d = (i - hd * (D / 4)) * 4;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            float Ls = 0.f, M = PKV_NEG_INF;
+            for (int z = x; z <= last; ++z) {
+                if (unit_at(z) < 0) continue;
+                const int pi = part_at(z);
+                const float f = factor[z * GP + hd];
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    pi < W ? cut + ((size_t)pi * p.g + hd) * D + d : ends + (pi - W) * (L::kPart / 4) + hd * L::kStride + d);
+                O.x = fmaf(v.x, f, O.x); O.y = fmaf(v.y, f, O.y); O.z = fmaf(v.z, f, O.z); O.w = fmaf(v.w, f, O.w);
+                Ls = fmaf(mL[pi * GP + hd], f, Ls);
+                M = fmaxf(M, mM[pi * GP + hd]);
+            }
+            if (begins && done) {
+                const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+                *reinterpret_cast<uint2 *>(p.out + (size_t)unit * p.g * D + hd * D + d) =
+                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+            } else {
+                *reinterpret_cast<float4 *>(rec + hd * D + d) = O;
+                if (d == 0) p.rec_ml[((size_t)blockIdx.x * 2 + begins) * p.g + hd] = make_float2(M, Ls);
+            }
+        }
+        if (!begins) { meta.x = unit; meta.y = done; }
+        else if (!done) meta.z = unit;
+        x = y;
+    }
+    if (tid == 0) p.meta[blockIdx.x] = meta;
+}
+
+// --------------------------------------------------------------- reduce ----
+// Where a unit begins in CTA c of the attention kernel and goes on past it,
+// that unit's records, c's second one and the first ones of the CTAs up to the
+// one where it ends, are merged by log-sum-exp.  Every CTA here looks through
+// the CTAs' notes and lists those units; the (unit, head) rows are dealt out to
+// the warps of the grid, or, of units with many records, to its CTAs.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeMany = 16;  // records from which a whole CTA takes a row
+constexpr int kMergeMaxCtas = 1184;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const StreamParams p, int ctas) {
+    constexpr int EPL = D / 32;
+    __shared__ int s_meta[kMergeMaxCtas][3];  // (unit of record 0, ends, unit of record 1)
+    __shared__ int2 s_few[kMergeMaxCtas], s_many[kMergeMaxCtas];  // (first CTA, records)
+    __shared__ int s_warp[2][kMergeWarps];
+    __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps], s_m[kMergeWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dependency_wait();
+    for (int i = tid; i < ctas; i += kMergeWarps * 32) {
+        const int4 m = p.meta[i];
+        s_meta[i][0] = m.x; s_meta[i][1] = m.y; s_meta[i][2] = m.z;
+    }
+    __syncthreads();
+    // in the line's order, which every CTA finds alike
+    int few = 0, many = 0;
+    for (int c0 = 0; c0 < ctas; c0 += kMergeWarps * 32) {
+        const int c = c0 + tid, unit = c < ctas ? s_meta[c][2] : -1;
+        int n = 0;
+        if (unit >= 0) {
+            int e = c + 1;
+            while (e < ctas - 1 && s_meta[e][0] == unit && !s_meta[e][1]) ++e;
+            n = min(e, ctas - 1) - c + 1;
+        }
+        const bool is_few = n > 0 && n <= kMergeMany, is_many = n > kMergeMany;
+        const uint32_t mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, is_many);
+        if (lane == 0) { s_warp[0][warp] = __popc(mf); s_warp[1][warp] = __popc(mm); }
+        __syncthreads();
+        int at_few = few + __popc(mf & ((1u << lane) - 1)), at_many = many + __popc(mm & ((1u << lane) - 1));
+        for (int w = 0; w < kMergeWarps; ++w) {
+            if (w < warp) { at_few += s_warp[0][w]; at_many += s_warp[1][w]; }
+            few += s_warp[0][w];
+            many += s_warp[1][w];
+        }
+        if (is_few) s_few[at_few] = make_int2(c, n);
+        if (is_many) s_many[at_many] = make_int2(c, n);
+        __syncthreads();
+    }
+    float acc[EPL], lsum, M;
+    // records first, first + step, ... of a row
+    auto merge = [&](int2 u, int head, int first, int step) {
+        auto record = [&](int i) { return ((size_t)(u.x + i) * 2 + (i == 0)) * p.g + head; };
+        M = PKV_NEG_INF;
+        for (int i = first + step * lane; i < u.y; i += step * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
+        M = warp_max_f32(M);
+        lsum = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = first; i < u.y; i += step) {
+            const size_t r = record(i);
+            const float2 ml = p.rec_ml[r];
+            const float f = ml.x == PKV_NEG_INF ? 0.f : ex2(ml.x - M);
+            lsum = fmaf(ml.y, f, lsum);
+            const float *a = p.rec_acc + r * D + lane * EPL;
+            if constexpr (EPL == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(a);
+                acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
+                acc[2] = fmaf(x.z, f, acc[2]); acc[3] = fmaf(x.w, f, acc[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(a);
+                acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
+            }
+        }
+    };
+    for (int i = blockIdx.x; i < many * p.g; i += gridDim.x) {
+        const int2 u = s_many[i / p.g];
+        const int head = i % p.g;
+        merge(u, head, warp, kMergeWarps);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
+        if (lane == 0) { s_l[warp] = lsum; s_m[warp] = M; }
+        __syncthreads();
+        if (tid < D) {
+            float T = PKV_NEG_INF, Ls = 0.f, O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) T = fmaxf(T, s_m[w]);
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) {
+                const float f = s_m[w] == PKV_NEG_INF ? 0.f : ex2(s_m[w] - T);
+                Ls = fmaf(s_l[w], f, Ls);
+                O = fmaf(s_o[w][tid], f, O);
+            }
+            p.out[((size_t)s_meta[u.x][2] * p.g + head) * D + tid] =
+                __float2bfloat16_rn(Ls > 0.f || Ls != Ls ? O / Ls : 0.f);
+        }
+        __syncthreads();
+    }
+    for (int i = blockIdx.x * kMergeWarps + warp; i < few * p.g; i += gridDim.x * kMergeWarps) {
+        const int2 u = s_few[i / p.g];
+        const int head = i % p.g;
+        merge(u, head, 0, 1);
+        const float inv = lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f;
+        __nv_bfloat16 *out = p.out + ((size_t)s_meta[u.x][2] * p.g + head) * D + lane * EPL;
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2)
+            *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+}  // namespace pkv

@@ -18,7 +18,7 @@
 #include "block_manager.cuh"
 #include "block_select.cuh"
 #include "decode.cuh"
-#include "decode_sparse.cuh"
+#include "decode_stream.cuh"
 #include "pkv.h"
 #include "prefill.cuh"
 #include "prefill_tc.cuh"
@@ -175,12 +175,12 @@ bool workspace_layout(int32_t B, int32_t Hq, int32_t D, int32_t max_ctx, int32_t
 
 // ---------------------------------------------------- decode dispatch ----
 
-template <int D, int PATH, int GS, int GPAD, bool KV8 = false, bool KVB = false>
+template <int D, int PATH, int GS, int GPAD, bool KV8 = false>
 pkv_status launch_decode(const pkv::DecodeParams &prm, const CUtensorMap &mk, const CUtensorMap &mv,
                          cudaStream_t stream, int dev) {
     constexpr int NS = PATH == 0 ? kStagesSimt : kStagesMma;
-    using L = pkv::DecodeSmem<D, (PATH == 0 ? GS : GPAD), NS, KV8, KVB>;
-    auto kernel = pkv::paged_decode_kernel<D, PATH, GS, GPAD, NS, KV8, KVB>;
+    using L = pkv::DecodeSmem<D, (PATH == 0 ? GS : GPAD), NS, KV8>;
+    auto kernel = pkv::paged_decode_kernel<D, PATH, GS, GPAD, NS, KV8>;
     // the shared-memory attribute is set before the occupancy query, so a
     // cached occupancy also means the attribute is set on this device
     static DeviceCache occ_cache{};
@@ -230,18 +230,6 @@ pkv_status dispatch_group(int g, const pkv::DecodeParams &prm, const CUtensorMap
     return launch_decode<D, 1, 1, 16>(prm, mk, mv, stream, dev);
 }
 
-// An FP8 pool.  g = 2 runs on the tensor cores too: over e4m3 codes the
-// CUDA-core body is issue-bound (a conversion and four unpacked FMAs per code
-// pair).
-template <int D, bool KVB>
-pkv_status dispatch_group_fp8(int g, const pkv::DecodeParams &prm, const CUtensorMap &mk, const CUtensorMap &mv,
-                              cudaStream_t stream, int dev) {
-    if (g == 1) return launch_decode<D, 0, 1, 1, true, KVB>(prm, mk, mv, stream, dev);
-    if (g <= 4) return launch_decode<D, 1, 1, 4, true, KVB>(prm, mk, mv, stream, dev);
-    if (g <= 8) return launch_decode<D, 1, 1, 8, true, KVB>(prm, mk, mv, stream, dev);
-    return launch_decode<D, 1, 1, 16, true, KVB>(prm, mk, mv, stream, dev);
-}
-
 // --------------------------------------------- block-sparse decode ----
 
 // A launch of clusters of `splits` CTAs, allowed to start its prologue while
@@ -279,44 +267,70 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
     return true;
 }
 
-constexpr int kSparseMaxSplits = 8;
+// ------------------------------------------------------- stream decode ----
 
-// CTAs of a (sequence, kv head): as many as fill the GPU's SMs four times,
-// while each still has 8 stages (two of every consumer warp).
-int sparse_splits(long long units, long long stages, int sms) {
-    int splits = 1;
-    while (splits < kSparseMaxSplits && units * splits < 4ll * sms && stages / (2 * splits) >= 8) splits *= 2;
-    return splits;
+constexpr int kStreamMaxCtas = pkv::kMergeMaxCtas;  // 8 for each of 148 SMs
+constexpr int kStreamMinStages = 2;  // of a warp, while there are fewer than fill the grid
+constexpr int kStreamRing = 12;      // stages of a CTA in flight (e4m3); 8 of bf16
+
+struct StreamLayout {
+    long long ctas;  // as many as can have work, at most kStreamMaxCtas
+    size_t off_ml, off_acc, off_cut, total;
+};
+
+bool stream_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, long long stages, StreamLayout *w) {
+    if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || stages < 0) return false;
+    const long long line = (long long)B * Hkv * stages;
+    w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * kStreamMinStages), kStreamMaxCtas));
+    const size_t heads = (size_t)w->ctas * 2 * (Hq / Hkv);
+    w->off_ml = round256((size_t)w->ctas * sizeof(int4));
+    w->off_acc = w->off_ml + round256(heads * sizeof(float2));
+    w->off_cut = w->off_acc + round256(heads * D * sizeof(float));
+    w->total = w->off_cut + round256(heads / 2 * pkv::kConsumerWarps * D * sizeof(float));
+    return true;
 }
 
-template <int D, int PATH, int GPAD, bool KV8>
-pkv_status launch_sparse(pkv::SparseParams prm, long long units, const CUtensorMap &mk, const CUtensorMap &mv,
-                         cudaStream_t stream) {
-    constexpr int NS = PATH == 0 ? kStagesSimt : kStagesMma;
-    using L = pkv::SparseSmem<D, GPAD, NS, KV8>;
-    auto kernel = pkv::sparse_decode_kernel<D, PATH, GPAD, NS, KV8>;
+template <int D, int GPAD, bool KV8, bool SEL>
+pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *workspace, const CUtensorMap &mk,
+                         const CUtensorMap &mv, cudaStream_t stream) {
+    constexpr int NS = KV8 ? kStreamRing : 8;
+    using L = pkv::StreamSmem<D, GPAD, NS, KV8>;
+    auto kernel = pkv::stream_decode_kernel<D, GPAD, NS, KV8, SEL>;
     const int dev = current_device();
-    static DeviceCache done{};
-    if (!allow_smem(kernel, done, dev)) return PKV_ECUDA;
-    const int spe = prm.bs / pkv::kStageTok;
-    const long long stages = (long long)prm.K * spe;
-    prm.splits = sparse_splits(units, stages, sm_count(dev));
-    const long long per = (stages + prm.splits - 1) / prm.splits;
-    prm.share = (int)std::min<long long>(prm.K, (per + spe - 1) / spe + 1);
-    const size_t smem = L::bytes(prm.share);
-    if (smem > kMaxDynamicSmem || units * prm.splits > 0x7fffffffll) return PKV_EUNSUPPORTED;
-    ClusterLaunch cl(units * prm.splits, pkv::kDecodeThreads, smem, prm.splits, stream);
-    if (cudaLaunchKernelEx(&cl.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
+    static DeviceCache occ_cache{};
+    int occ = (dev >= 0 && dev < kMaxDevices) ? occ_cache[dev].load(std::memory_order_acquire) : 0;
+    if (occ == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
+            return PKV_ECUDA;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, pkv::kDecodeThreads, L::kBytes) != cudaSuccess ||
+            occ <= 0)
+            return PKV_ECUDA;
+        if (dev >= 0 && dev < kMaxDevices) occ_cache[dev].store(occ, std::memory_order_release);
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    prm.meta = reinterpret_cast<int4 *>(ws);
+    prm.rec_ml = reinterpret_cast<float2 *>(ws + wl.off_ml);
+    prm.rec_acc = reinterpret_cast<float *>(ws + wl.off_acc);
+    prm.cut = reinterpret_cast<float *>(ws + wl.off_cut);
+    prm.min_stages = kStreamMinStages;
+    const int ctas = (int)std::min<long long>(wl.ctas, (long long)sm_count(dev) * occ);
+    ClusterLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, 1, stream);
+    if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
+    if (ctas > 1) {
+        // a warp for each row that can have been cut, up to two CTAs an SM
+        const long long rows = ((long long)ctas * prm.g + pkv::kMergeWarps - 1) / pkv::kMergeWarps;
+        ClusterLaunch re(std::min<long long>(rows, 2ll * sm_count(dev)), pkv::kMergeWarps * 32, 0, 1, stream);
+        if (cudaLaunchKernelEx(&re.cfg, pkv::stream_reduce_kernel<D>, prm, ctas) != cudaSuccess) return PKV_ECUDA;
+    }
     return launch_status();
 }
 
-template <int D, bool KV8>
-pkv_status dispatch_sparse(const pkv::SparseParams &prm, long long units, const CUtensorMap &mk, const CUtensorMap &mv,
-                           cudaStream_t stream) {
-    if (prm.g == 1) return launch_sparse<D, 0, 1, KV8>(prm, units, mk, mv, stream);
-    if (prm.g <= 4) return launch_sparse<D, 1, 4, KV8>(prm, units, mk, mv, stream);
-    if (prm.g <= 8) return launch_sparse<D, 1, 8, KV8>(prm, units, mk, mv, stream);
-    return launch_sparse<D, 1, 16, KV8>(prm, units, mk, mv, stream);
+template <int D, bool KV8, bool SEL>
+pkv_status dispatch_stream(const pkv::StreamParams &prm, const StreamLayout &wl, void *ws, const CUtensorMap &mk,
+                           const CUtensorMap &mv, cudaStream_t stream) {
+    if (prm.g <= 4) return launch_stream<D, 4, KV8, SEL>(prm, wl, ws, mk, mv, stream);
+    if (prm.g <= 8) return launch_stream<D, 8, KV8, SEL>(prm, wl, ws, mk, mv, stream);
+    return launch_stream<D, 16, KV8, SEL>(prm, wl, ws, mk, mv, stream);
 }
 
 // Blocks of a (sequence, kv head) at most, and the parts of the workspace: the
@@ -570,11 +584,10 @@ pkv_status check_pairs(const int32_t *src_dst_pairs, int32_t num_pairs, int32_t 
     return PKV_OK;
 }
 
-// Decode over a bf16 pool (scales null) or an FP8 (e4m3) pool: with per-kv-head
-// dequantisation scales (head dim 128), or, `block_scales`, with one for each
-// block and kv head.
+// Decode over a bf16 pool (scales null) or an FP8 (e4m3) pool with per-kv-head
+// dequantisation scales (head dim 128).
 pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
-                       const float *v_scale, bool block_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                       const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq,
                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
                        int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
                        int32_t partition_tokens, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
@@ -587,7 +600,7 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     if (num_kv_heads != pool.num_kv_heads || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
     const int g = num_q_heads / num_kv_heads;
     if (g > 16) return PKV_EUNSUPPORTED;
-    if (kv8 && !block_scales && pool.head_dim != 128) return PKV_EUNSUPPORTED;
+    if (kv8 && pool.head_dim != 128) return PKV_EUNSUPPORTED;
     if (partition_tokens < 0 || partition_tokens % 16 != 0 || partition_tokens > 65536) return PKV_EINVAL;
     if (num_seqs == 0) return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace) return PKV_EINVAL;
@@ -623,13 +636,8 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     prm.maxP = (int)std::max<long long>(1, ((long long)max_context_len + PT - 1) / PT);
     prm.pool_rows = pool.num_blocks * pool.num_kv_heads * pool.block_size;
     prm.scale_log2 = scale * 1.4426950408889634f;
-    if (block_scales) {
-        prm.kb_scales = k_scale;
-        prm.vb_scales = v_scale;
-    } else {
-        prm.k_scale = k_scale;
-        prm.v_scale = v_scale;
-    }
+    prm.k_scale = k_scale;
+    prm.v_scale = v_scale;
 
     CUtensorMap mk, mv;
     if (kv8) {
@@ -643,10 +651,14 @@ pkv_status decode_impl(const void *q, const void *k_cache, const void *v_cache, 
     pkv_status r = launch_status();
     if (r != PKV_OK) return r;
     const int dev = current_device();
-    if (block_scales)
-        return D == 128 ? dispatch_group_fp8<128, true>(g, prm, mk, mv, st, dev)
-                        : dispatch_group_fp8<64, true>(g, prm, mk, mv, st, dev);
-    if (kv8) return dispatch_group_fp8<128, false>(g, prm, mk, mv, st, dev);
+    if (kv8) {
+        // g = 2 runs on the tensor cores too: over e4m3 codes the CUDA-core body
+        // is issue-bound (a conversion and four unpacked FMAs per code pair)
+        if (g == 1) return launch_decode<128, 0, 1, 1, true>(prm, mk, mv, st, dev);
+        if (g <= 4) return launch_decode<128, 1, 1, 4, true>(prm, mk, mv, st, dev);
+        if (g <= 8) return launch_decode<128, 1, 1, 8, true>(prm, mk, mv, st, dev);
+        return launch_decode<128, 1, 1, 16, true>(prm, mk, mv, st, dev);
+    }
     return D == 128 ? dispatch_group<128>(g, prm, mk, mv, st, dev) : dispatch_group<64>(g, prm, mk, mv, st, dev);
 }
 
@@ -766,7 +778,7 @@ pkv_status paged_attn_decode(const void *q, const void *k_cache, const void *v_c
                              int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out, pkv_pool pool,
                              int32_t max_context_len, int32_t partition_tokens, void *workspace,
                              size_t workspace_bytes, pkv_stream_t stream) {
-    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_tables, max_blocks_per_seq, context_lens,
+    return decode_impl(q, k_cache, v_cache, nullptr, nullptr, block_tables, max_blocks_per_seq, context_lens,
                        num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
                        workspace, workspace_bytes, stream);
 }
@@ -778,7 +790,7 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
                                  int32_t partition_tokens, void *workspace, size_t workspace_bytes,
                                  pkv_stream_t stream) {
     if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return PKV_EINVAL;
-    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, false, block_tables, max_blocks_per_seq, context_lens,
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq, context_lens,
                        num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
                        workspace, workspace_bytes, stream);
 }
@@ -814,16 +826,61 @@ pkv_status pkv_write_fp8(const void *k, const void *v, const int64_t *slot_mappi
     return launch_status();
 }
 
+size_t pkv_decode_fp8_block_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_context_len) {
+    if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || max_context_len < 0) return 0;
+    StreamLayout w;
+    const long long stages = ((long long)max_context_len + pkv::kStageTok - 1) / pkv::kStageTok;
+    return stream_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, stages, &w) ? w.total : 0;
+}
+
 pkv_status paged_attn_decode_fp8_block(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
                                        const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
                                        int32_t num_kv_heads, void *out, pkv_pool pool, int32_t max_context_len,
-                                       int32_t partition_tokens, void *workspace, size_t workspace_bytes,
-                                       pkv_stream_t stream) {
-    if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4)) return PKV_EINVAL;
-    return decode_impl(q, k_cache, v_cache, k_scales, v_scales, true, block_tables, max_blocks_per_seq, context_lens,
-                       num_seqs, num_q_heads, scale, num_kv_heads, out, pool, max_context_len, partition_tokens,
-                       workspace, workspace_bytes, stream);
+                                       void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    const pkv_status ps = check_pool(pool);
+    if (ps != PKV_OK) return ps;
+    if (pool.kv_dtype != PKV_KV_E4M3) return PKV_EINVAL;
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
+        return PKV_EINVAL;
+    if (num_kv_heads != pool.num_kv_heads || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+    const int g = num_q_heads / num_kv_heads;
+    if (g > 16 || (long long)num_seqs * num_kv_heads >= (1ll << 31)) return PKV_EUNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens || !out || !workspace)
+        return PKV_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(workspace, 256))
+        return PKV_EINVAL;
+    StreamLayout wl;
+    const long long stages = ((long long)max_context_len + pkv::kStageTok - 1) / pkv::kStageTok;
+    if (!stream_layout(num_seqs, num_q_heads, num_kv_heads, pool.head_dim, stages, &wl) || workspace_bytes < wl.total)
+        return PKV_EINVAL;
+    pkv::StreamParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.B = num_seqs;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.g = g;
+    p.MBS = max_blocks_per_seq;
+    p.bs = pool.block_size;
+    p.NB = pool.num_blocks;
+    p.max_ctx = max_context_len;
+    p.pool_rows = pool.num_blocks * pool.num_kv_heads * pool.block_size;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    CUtensorMap mk, mv;
+    if (!encode_pool_map_u8(&mk, k_cache, pool) || !encode_pool_map_u8(&mv, v_cache, pool)) return PKV_ECUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return pool.head_dim == 128 ? dispatch_stream<128, true, false>(p, wl, workspace, mk, mv, st)
+                                : dispatch_stream<64, true, false>(p, wl, workspace, mk, mv, st);
 }
 
 pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *block_tables, int32_t max_blocks_per_seq,
@@ -977,11 +1034,19 @@ pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *b
     return pool.head_dim == 128 ? launch_select<128>(p, units, st) : launch_select<64>(p, units, st);
 }
 
+size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int32_t num_selected) {
+    if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || block_size <= 0 || num_selected <= 0) return 0;
+    StreamLayout w;
+    const long long stages = (long long)num_selected * ((block_size + pkv::kStageTok - 1) / pkv::kStageTok);
+    return stream_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, stages, &w) ? w.total : 0;
+}
+
 pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
                                     const float *v_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                     const int32_t *context_lens, const int32_t *selected, int32_t num_selected,
                                     int32_t num_seqs, int32_t num_q_heads, float scale, int32_t num_kv_heads, void *out,
-                                    pkv_pool pool, pkv_stream_t stream) {
+                                    pkv_pool pool, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
     const pkv_status ps = check_pool(pool);
     if (ps != PKV_OK) return ps;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
@@ -990,14 +1055,23 @@ pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const vo
     const bool kv8 = pool.kv_dtype == PKV_KV_E4M3;
     if (kv8 != (k_scales != nullptr) || kv8 != (v_scales != nullptr)) return PKV_EINVAL;
     const int g = num_q_heads / num_kv_heads;
-    if (g > 16 || (long long)num_selected * pool.block_size >= (1ll << 31)) return PKV_EUNSUPPORTED;
+    if (g > 16 || (long long)num_selected * pool.block_size >= (1ll << 31) ||
+        (long long)num_seqs * num_kv_heads >= (1ll << 31))
+        return PKV_EUNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
-    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !selected || !out) return PKV_EINVAL;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !selected || !out || !workspace)
+        return PKV_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(selected, 4) || !aligned(k_scales, 4) ||
-        !aligned(v_scales, 4))
+        !aligned(v_scales, 4) || !aligned(workspace, 256))
         return PKV_EINVAL;
-    pkv::SparseParams p;
+    StreamLayout wl;
+    if (!stream_layout(num_seqs, num_q_heads, num_kv_heads, pool.head_dim,
+                       (long long)num_selected * (pool.block_size / pkv::kStageTok), &wl) ||
+        workspace_bytes < wl.total)
+        return PKV_EINVAL;
+    pkv::StreamParams p;
+    std::memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.block_tables = block_tables;
@@ -1012,6 +1086,8 @@ pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const vo
     p.bs = pool.block_size;
     p.NB = pool.num_blocks;
     p.K = num_selected;
+    p.B = num_seqs;
+    p.max_ctx = 0x7fffffff;  // the table's length bounds the contexts
     p.pool_rows = pool.num_blocks * pool.num_kv_heads * pool.block_size;
     p.scale_log2 = scale * 1.4426950408889634f;
     CUtensorMap mk, mv;
@@ -1020,11 +1096,12 @@ pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const vo
     } else if (!encode_pool_map(&mk, k_cache, pool) || !encode_pool_map(&mv, v_cache, pool)) {
         return PKV_ECUDA;
     }
-    const long long units = (long long)num_seqs * num_kv_heads;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (pool.head_dim == 128)
-        return kv8 ? dispatch_sparse<128, true>(p, units, mk, mv, st) : dispatch_sparse<128, false>(p, units, mk, mv, st);
-    return kv8 ? dispatch_sparse<64, true>(p, units, mk, mv, st) : dispatch_sparse<64, false>(p, units, mk, mv, st);
+        return kv8 ? dispatch_stream<128, true, true>(p, wl, workspace, mk, mv, st)
+                   : dispatch_stream<128, false, true>(p, wl, workspace, mk, mv, st);
+    return kv8 ? dispatch_stream<64, true, true>(p, wl, workspace, mk, mv, st)
+               : dispatch_stream<64, false, true>(p, wl, workspace, mk, mv, st);
 }
 
 size_t pkv_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

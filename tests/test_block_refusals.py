@@ -61,7 +61,7 @@ def test_key_bounds_refuses(change, status):
 
 def decode8(**kw):
     a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, tables=FAKE, mbs=4, ctx=FAKE, B=2, Hq=4, scale=0.1, Hkv=2,
-             out=FAKE, pool=pool(), max_ctx=64, pt=0, ws=FAKE, ws_bytes=1 << 30)
+             out=FAKE, pool=pool(), max_ctx=64, ws=FAKE, ws_bytes=1 << 30)
     a.update(kw)
     return pkv.load_library().paged_attn_decode_fp8_block(*a.values(), None)
 
@@ -69,7 +69,7 @@ def decode8(**kw):
 @pytest.mark.parametrize("change,status", [
     ({"B": 0}, 0), ({"B": -1}, EINVAL), ({"Hq": 5}, EINVAL), ({"Hq": 34}, EUNSUP), ({"Hkv": 4, "Hq": 8}, EINVAL),
     ({"pool": pool(dtype=0)}, EINVAL), ({"pool": pool(d=256)}, EUNSUP), ({"max_ctx": -1}, EINVAL), ({"mbs": 0}, EINVAL),
-    ({"pt": 24}, EINVAL), ({"ws_bytes": 16}, EINVAL), ({"ws": ODD16}, EINVAL),
+    ({"ws_bytes": 16}, EINVAL), ({"ws": ODD16}, EINVAL),
     *[({n: None}, EINVAL) for n in ("q", "kc", "vc", "ks", "vs", "tables", "ctx", "out", "ws")],
     *[({n: ODD16}, EINVAL) for n in ("q", "kc", "vc", "out")],
     *[({n: ODD4}, EINVAL) for n in ("ks", "vs", "tables", "ctx")],
@@ -137,7 +137,7 @@ def test_select_refuses(change, status):
 
 def sparse(**kw):
     a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, tables=FAKE, mbs=4, ctx=FAKE, sel=FAKE, K=4, B=2, Hq=4,
-             scale=0.1, Hkv=2, out=FAKE, pool=pool())
+             scale=0.1, Hkv=2, out=FAKE, pool=pool(), ws=FAKE, ws_bytes=1 << 30)
     a.update(kw)
     return pkv.load_library().paged_attn_decode_sparse(*a.values(), None)
 
@@ -147,7 +147,8 @@ def sparse(**kw):
     ({"K": 0}, EINVAL), ({"K": 1 << 27}, EUNSUP), ({"mbs": 0}, EINVAL), ({"pool": pool(d=256)}, EUNSUP),
     ({"ks": None}, EINVAL), ({"vs": None}, EINVAL), ({"pool": pool(dtype=0)}, EINVAL),  # scales go with an e4m3 pool
     ({"ks": None, "pool": pool(dtype=0)}, EINVAL), ({"pool": pool(dtype=3)}, EINVAL),
-    *[({n: None}, EINVAL) for n in ("q", "kc", "vc", "tables", "ctx", "sel", "out")],
+    *[({n: None}, EINVAL) for n in ("q", "kc", "vc", "tables", "ctx", "sel", "out", "ws")],
+    ({"ws_bytes": 16}, EINVAL), ({"ws": ODD16}, EINVAL),
     *[({n: ODD16}, EINVAL) for n in ("q", "kc", "vc", "out")],
     *[({n: ODD4}, EINVAL) for n in ("ks", "vs", "tables", "ctx", "sel")],
 ])
