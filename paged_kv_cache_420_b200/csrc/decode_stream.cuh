@@ -3,14 +3,15 @@
 //
 // All 16-token stages of all (sequence, kv head) units form one line,
 // sequence-major, and every consumer warp of the grid takes one contiguous
-// stretch of it, all of the same length to a stage: no plan kernel, no work
-// counter, no partition size, and nothing is left for a tail however the
-// lengths are spread, from one long sequence to thousands of short ones.  A
-// warp runs through the units of its stretch with one softmax state.  A unit
+// stretch of it, all of the same cost (a stage counts 1, a unit kUnitCost more
+// for its q, its first maxima and its output): no plan kernel, no work counter
+// and no partition size, however the lengths are spread, from one long
+// sequence to thousands of short ones.  A warp runs through the units of its stretch with one softmax state.  A unit
 // that lies within a stretch is written out by its warp; the parts of a unit
 // that stretches cut are merged in two steps, within the CTA (whose four
 // stretches are neighbours), then, where a unit goes on over CTAs, through at
-// most two records of each CTA that a second kernel merges.
+// most two records of each CTA that a second kernel merges.  Where all units
+// are short, the stretches end between units, and there is nothing to merge.
 //
 //   dense:    unit (s, h) has ceil(context / 16) stages; each CTA adds up the
 //             contexts itself (they are few, and in L2)
@@ -362,6 +363,7 @@ struct TileState {
 
 // ------------------------------------------------------------------- work ----
 
+constexpr int kUnitCost = 2;     // of a unit, in stages
 constexpr int kStreamGroup = 8;  // stages that a stretch's lanes look up at once
 static_assert(kConsumerWarps * kStreamGroup == 32, "a lane of the producer for each stage of a group");
 
@@ -374,20 +376,28 @@ struct StreamParams {
     const float *k_scales;        // [NB][Hkv] (e4m3 pool)
     const float *v_scales;
     float *cut;                   // workspace: [CTAs][W][g][D], the parts at the beginnings of warps' stretches
-    int4 *meta;                   // workspace: [CTAs] (unit of record 0 or -1, whether the unit ends there, unit of record 1 or -1)
+    int2 *meta;                   // workspace: [CTAs] (a unit that ends in the CTA and began in another, or -1; that CTA)
     float2 *rec_ml;               // workspace: [CTAs][2][g] = (m, l)
     float *rec_acc;               // workspace: [CTAs][2][g][D]
     int B, Hq, Hkv, g, MBS, bs, NB, K, max_ctx;
     int pool_rows;
-    int min_stages;  // of a stretch, while there are fewer stages than fill the grid
+    int min_cost;    // of a stretch, while there is less work than fills the grid
+    int whole;       // stretches end between units
     float scale_log2;
 };
 
-// A part of a unit that a warp leaves behind: the unit, and whether the unit
-// begins and ends in it.
+// A part of a unit that a warp leaves behind.
 struct StreamPart {
-    short begins, ends;
     int unit;
+    int from;  // the CTA in which the unit began, if it ends in this part; else -1
+    int begins;  // whether the unit begins in this part
+};
+
+// Where a stretch begins: a stage of the line, the sequence it lies in, and the
+// stages and the cost of the line before that sequence.
+struct StreamBound {
+    long long x, base, cost_base;
+    int seq;
 };
 
 // What a consumer has to know of a stage.
@@ -395,7 +405,7 @@ struct __align__(16) StreamStage {
     int unit;
     int valid;  // tokens; 0: none (nothing was loaded)
     int first;  // the first of its unit in this stretch: fresh state, q in the slot
-    int last;   // the last: 0 no, 1 the unit is complete, 2 its beginning was cut off (3: and it ends here), 4 its end is cut off
+    int last;   // the last: 0 no, 1 the unit is complete, 2 its beginning was cut off, 4 its end is cut off, 8 + c: it began in CTA c and ends here
 };
 
 template <int D, int GP, int NS, bool KV8>
@@ -414,12 +424,14 @@ struct StreamSmem {
     static constexpr int oL = oM + 2 * kW * GP * 4;
     static constexpr int oFactor = oL + 2 * kW * GP * 4;
     static constexpr int oPartInfo = oFactor + 2 * kW * GP * 4;         // StreamPart [2 W]
-    static constexpr int oBars = (oPartInfo + 2 * kW * 8 + 7) / 8 * 8;
+    static constexpr int oGroups = oPartInfo + 2 * kW * (int)sizeof(StreamPart);  // int [1 + 2 W]: neighbouring parts of one unit
+    static constexpr int oBars = (oGroups + (1 + 2 * kW) * 4 + 7) / 8 * 8;
     static constexpr int oScales = oBars + 2 * NS * 8;
     static constexpr int oInfo = (oScales + (KV8 ? NS * 8 : 0) + 15) / 16 * 16;
-    static constexpr int oScan = oInfo + NS * 16;                       // long long [threads]
-    static constexpr int oWarpSum = oScan + kDecodeThreads * 8;
-    static constexpr int oAbort = oWarpSum + 8 * 8;
+    static constexpr int oScan = oInfo + NS * 16;                       // long long [threads][2]: stages, cost
+    static constexpr int oWarpSum = oScan + kDecodeThreads * 16;
+    static constexpr int oBounds = oWarpSum + (kW + 1) * 16;            // StreamBound [W + 1]
+    static constexpr int oAbort = oBounds + (kW + 1) * (int)sizeof(StreamBound);
     static constexpr int kBytes = oAbort + 16;
     static_assert(kW * kPart <= NS * kStage, "the parts at the stretches' ends fit into the rings");
 };
@@ -427,7 +439,7 @@ struct StreamSmem {
 // CTAs of an SM that the registers must allow.
 constexpr int stream_min_ctas(int GPAD, bool KV8) { return GPAD > 8 ? 2 : KV8 ? 4 : 3; }
 
-// Where a CTA's and a warp's stretch begins: `total` stages over `parts`.
+// Where part i of `parts` of a line of cost `total` begins.
 __device__ __forceinline__ long long stretch_begin(long long total, int parts, int i) {
     return (total / parts) * i + (total % parts) * i / parts;
 }
@@ -451,8 +463,10 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
     StreamPart *part_info = reinterpret_cast<StreamPart *>(smem + L::oPartInfo);
     float *mM = reinterpret_cast<float *>(smem + L::oM);
     float *mL = reinterpret_cast<float *>(smem + L::oL);
-    long long *scan = reinterpret_cast<long long *>(smem + L::oScan);
-    long long *warp_sum = reinterpret_cast<long long *>(smem + L::oWarpSum);
+    int *groups = reinterpret_cast<int *>(smem + L::oGroups);
+    longlong2 *scan = reinterpret_cast<longlong2 *>(smem + L::oScan);
+    longlong2 *warp_sum = reinterpret_cast<longlong2 *>(smem + L::oWarpSum);
+    StreamBound *bounds = reinterpret_cast<StreamBound *>(smem + L::oBounds);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::oAbort);
     const uint32_t tiles = smem_u32(smem + L::oTiles);
     float *factor = reinterpret_cast<float *>(smem + L::oFactor);
@@ -487,31 +501,38 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
     };
     const int spe = p.bs / kStageTok;  // stages of a block
     const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;  // sequences whose stages a thread adds up
-    long long total;
+    auto stages_of = [&](int n) { return (n + kStageTok - 1) / kStageTok; };
+    longlong2 total;  // stages, cost
     if constexpr (SEL) {
-        total = (long long)p.B * p.Hkv * p.K * spe;
+        total.x = total.y = (long long)p.B * p.Hkv * p.K * spe;
         if (blockIdx.x == 0)
             for (int s = tid; s < p.B; s += kDecodeThreads) context(s, true);
     } else {
-        long long sum = 0;
-        for (int s = tid * per; s < min(p.B, (tid + 1) * per); ++s)
-            sum += (context(s, blockIdx.x == 0) + kStageTok - 1) / kStageTok;
-        sum *= p.Hkv;
-        long long incl = sum;
+        longlong2 sum = make_longlong2(0, 0);
+        for (int s = tid * per; s < min(p.B, (tid + 1) * per); ++s) {
+            const int nst = stages_of(context(s, blockIdx.x == 0));
+            sum.x += nst;
+            sum.y += nst > 0 ? nst + kUnitCost : 0;
+        }
+        sum.x *= p.Hkv;
+        sum.y *= p.Hkv;
+        longlong2 incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            const long long x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+            if (lane >= o) { incl.x += x; incl.y += y; }
         }
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        long long before = 0;
-        total = 0;
+        longlong2 before = make_longlong2(0, 0);
+        total = before;
         for (int w = 0; w <= W; ++w) {
-            before += w < warp ? warp_sum[w] : 0;
-            total += warp_sum[w];
+            if (w < warp) { before.x += warp_sum[w].x; before.y += warp_sum[w].y; }
+            total.x += warp_sum[w].x;
+            total.y += warp_sum[w].y;
         }
-        scan[tid] = before + incl - sum;  // the stages before this thread's sequences
+        // what lies before this thread's sequences
+        scan[tid] = make_longlong2(before.x + incl.x - sum.x, before.y + incl.y - sum.y);
         // empty sequences get a zero row
         const int vec = p.Hq * D / 8;
         for (int s = blockIdx.x; s < p.B; s += gridDim.x)
@@ -519,37 +540,60 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 for (int i = tid; i < vec; i += kDecodeThreads)
                     reinterpret_cast<uint4 *>(p.out)[(size_t)s * vec + i] = make_uint4(0, 0, 0, 0);
     }
-    __syncthreads();
-    const int ctas = (int)max(1ll, min((long long)gridDim.x, total / (W * p.min_stages)));
-    if ((int)blockIdx.x >= ctas || total == 0) {
-        if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, -1, 0);
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, total.y / (W * p.min_cost)));
+    if ((int)blockIdx.x >= ctas || total.x == 0) {
+        if (tid == 0) p.meta[blockIdx.x] = make_int2(-1, 0);
         return;
     }
-    const long long A = stretch_begin(total, ctas, blockIdx.x), E = stretch_begin(total, ctas, blockIdx.x + 1);
-    auto warp_begin = [&](int w) { return A + (E - A) * w / W; };
+    __syncthreads();
+    // The bounds of the warps' stretches: thread t finds the stage at cost y.
+    if (tid <= W) {
+        const long long A = stretch_begin(total.y, ctas, blockIdx.x), E = stretch_begin(total.y, ctas, blockIdx.x + 1);
+        const long long y = A + (E - A) * tid / W;
+        StreamBound bd;
+        if constexpr (SEL) {
+            bd.x = y;
+            bd.seq = 0;
+            bd.base = bd.cost_base = 0;
+        } else {
+            int lo = 0, hi = kDecodeThreads - 1;  // the last thread whose sequences begin at or before y
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (scan[mid].y <= y) lo = mid; else hi = mid - 1;
+            }
+            bd.seq = min(lo * per, p.B - 1);
+            bd.base = scan[lo].x;
+            bd.cost_base = scan[lo].y;
+            bd.x = total.x;
+            for (int s = bd.seq; s < p.B && y < total.y; ++s) {
+                const int nst = stages_of(context(s, false)), cost = nst > 0 ? nst + kUnitCost : 0;
+                const long long off = y - bd.cost_base;
+                if (off < (long long)cost * p.Hkv) {
+                    const int h = (int)(off / cost), in = (int)(off - (long long)h * cost);
+                    const int i = p.whole ? (2 * in > cost ? nst : 0) : max(0, in - kUnitCost);
+                    bd.seq = s;
+                    bd.x = bd.base + (long long)h * nst + i;
+                    break;
+                }
+                bd.base += (long long)nst * p.Hkv;
+                bd.cost_base += (long long)cost * p.Hkv;
+            }
+        }
+        bounds[tid] = bd;
+    }
+    __syncthreads();
 
     if (warp == W) {
         // ------------------------------------------------------ producer --
         const int j = lane / kStreamGroup, sub = lane % kStreamGroup;
-        const long long a = warp_begin(j), b = warp_begin(j + 1);
+        const long long a = bounds[j].x, b = bounds[j + 1].x;
         const int len = (int)(b - a);
         int longest = len;
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, 8));
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, 16));
-        // dense: this lane's sequence and the line's stages before it
-        int cs = 0, nst = 0, n = 0;
-        long long base = 0;
-        if constexpr (!SEL) {
-            int lo = 0, hi = kDecodeThreads - 1;  // the last thread whose sequences begin at or before a
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (scan[mid] <= a) lo = mid; else hi = mid - 1;
-            }
-            cs = min(lo * per, p.B - 1);
-            base = scan[lo];
-            n = context(cs, false);
-            nst = (n + kStageTok - 1) / kStageTok;
-        }
+        // dense: this lane's sequence, and the line before it
+        int cs = bounds[j].seq, n = SEL ? 0 : context(cs, false), nst = stages_of(n);
+        long long base = bounds[j].base, cost_base = bounds[j].cost_base;
         struct Stage {
             StreamStage st;
             int row;
@@ -571,8 +615,9 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
             } else {
                 while (x >= base + (long long)nst * p.Hkv) {
                     base += (long long)nst * p.Hkv;
+                    cost_base += nst > 0 ? (long long)(nst + kUnitCost) * p.Hkv : 0;
                     n = context(++cs, false);
-                    nst = (n + kStageTok - 1) / kStageTok;
+                    nst = stages_of(n);
                 }
                 s = cs;
                 len_u = nst;
@@ -586,7 +631,14 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
             if (r.st.first)  // its q, for the consumer's loads
                 for (int y = 0; y < p.g * D * 2; y += 128)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(p.q) + (size_t)r.st.unit * p.g * D * 2 + y));
-            r.st.last = i == len_u - 1 || k == len - 1 ? (begins ? (ends ? 1 : 4) : (ends ? 3 : 2)) : 0;
+            r.st.last = i == len_u - 1 || k == len - 1 ? (begins ? (ends ? 1 : 4) : 2) : 0;
+            if (r.st.last == 2 && ends) {
+                // it began in the last CTA whose bound is not behind its first stage
+                const long long y0 = SEL ? x - i : cost_base + (long long)h * (len_u + kUnitCost) + kUnitCost;
+                int c = (int)min((long long)ctas - 1, (long long)((double)y0 / (double)total.y * ctas) + 1);
+                while (c > 0 && stretch_begin(total.y, ctas, c) > y0) --c;
+                r.st.last = 8 + c;
+            }
             int blk = i / spe, off_blk = (i - blk * spe) * kStageTok;  // logical block, token in it
             if constexpr (SEL) {
                 n = context(s, false);
@@ -656,11 +708,15 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 if (k % kStreamGroup == sub) mbar_wait_bounded(&full[j * DEPTH + k % DEPTH], (k / DEPTH) & 1, kWaitLimitNs);
     } else {
         // ------------------------------------------------------ consumer --
-        const int len = (int)(warp_begin(warp + 1) - warp_begin(warp));
+        const int len = (int)(bounds[warp + 1].x - bounds[warp].x);
         TileState<D, NT, KV8> state;
         auto store_part = [&](int i, float *acc, int stride, const StreamStage &st) {
             state.store_part(acc, stride, mM + i * GP, mL + i * GP, lane, p.g);
-            if (lane == 0) { part_info[i].unit = st.unit; part_info[i].begins = st.last == 4; part_info[i].ends = st.last == 3; }
+            if (lane == 0) {
+                part_info[i].unit = st.unit;
+                part_info[i].begins = st.last == 4;
+                part_info[i].from = st.last >= 8 ? st.last - 8 : -1;
+            }
         };
         StreamStage tail;
         tail.unit = -1; tail.last = 0;
@@ -702,95 +758,94 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
     grid_launch_dependents();
 
     // The parts in the line's order: warp 0's first, warp 0's last, warp 1's
-    // first, ...  Neighbours of one unit belong together.  Thread (x, head)
-    // works out part x's factor, and its group's sums if it is the first.
+    // first, ...  Neighbours of one unit form a group.  Thread (x, head) works
+    // out part x's factor in its group, a warp lists the groups.
     auto part_at = [&](int x) { return (x >> 1) + (x & 1) * W; };
-    auto unit_at = [&](int x) { return part_info[part_at(x)].unit; };
+    if (warp == W) {
+        const int x = lane & (2 * W - 1), unit = part_info[part_at(x)].unit;
+        const uint32_t some = __ballot_sync(0xffffffffu, unit >= 0) & ((1u << (2 * W)) - 1);
+        const uint32_t below = some & ((1u << x) - 1);
+        const int prev = __shfl_sync(0xffffffffu, unit, below ? 31 - __clz(below) : 0);
+        const uint32_t first = __ballot_sync(0xffffffffu, unit >= 0 && !(below && prev == unit)) & ((1u << (2 * W)) - 1);
+        if (lane < 2 * W && ((first >> x) & 1u)) groups[1 + __popc(first & ((1u << x) - 1))] = x;
+        if (lane == 0) groups[0] = __popc(first);
+    }
     for (int i = tid; i < 2 * W * p.g; i += kDecodeThreads) {
-        const int x = i / p.g, hd = i - x * p.g, unit = unit_at(x);
+        const int x = i / p.g, hd = i - x * p.g, unit = part_info[part_at(x)].unit;
         if (unit < 0) continue;
         float M = PKV_NEG_INF;
 #pragma unroll
         for (int y = 0; y < 2 * W; ++y)
-            if (unit_at(y) == unit) M = fmaxf(M, mM[part_at(y) * GP + hd]);
+            if (part_info[y].unit == unit) M = fmaxf(M, mM[y * GP + hd]);
         const float mu = mM[part_at(x) * GP + hd];
         factor[x * GP + hd] = mu == PKV_NEG_INF ? 0.f : ex2(mu - M);
     }
+    if (tid == 0) p.meta[blockIdx.x] = make_int2(-1, 0);
     __syncthreads();
-    int4 meta = make_int4(-1, 0, -1, 0);
-    for (int x = 0; x < 2 * W;) {
-        const int unit = unit_at(x);
-        if (unit < 0) { ++x; continue; }
-        int y = x + 1, last = x;  // parts x .. last (others than `unit` among them: none)
-        for (; y < 2 * W && (unit_at(y) < 0 || unit_at(y) == unit); ++y)
-            if (unit_at(y) == unit) last = y;
-        // a group that does not begin with its unit goes back before the CTA
-        const bool begins = part_info[part_at(x)].begins != 0, done = part_info[part_at(last)].ends != 0;
-        float *rec = p.rec_acc + ((size_t)blockIdx.x * 2 + begins) * p.g * D;
-        for (int i = tid; i < p.g * D / 4; i += kDecodeThreads) {
-            const int hd = i / (D / 4), d = (i - hd * (D / 4)) * 4;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            float Ls = 0.f, M = PKV_NEG_INF;
-            for (int z = x; z <= last; ++z) {
-                if (unit_at(z) < 0) continue;
-                const int pi = part_at(z);
-                const float f = factor[z * GP + hd];
-                const float4 v = *reinterpret_cast<const float4 *>(
-                    pi < W ? cut + ((size_t)pi * p.g + hd) * D + d : ends + (pi - W) * (L::kPart / 4) + hd * L::kStride + d);
-                O.x = fmaf(v.x, f, O.x); O.y = fmaf(v.y, f, O.y); O.z = fmaf(v.z, f, O.z); O.w = fmaf(v.w, f, O.w);
-                Ls = fmaf(mL[pi * GP + hd], f, Ls);
-                M = fmaxf(M, mM[pi * GP + hd]);
-            }
-            if (begins && done) {
-                const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-                *reinterpret_cast<uint2 *>(p.out + (size_t)unit * p.g * D + hd * D + d) =
-                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
-            } else {
-                *reinterpret_cast<float4 *>(rec + hd * D + d) = O;
-                if (d == 0) p.rec_ml[((size_t)blockIdx.x * 2 + begins) * p.g + hd] = make_float2(M, Ls);
-            }
+    const int quads = p.g * D / 4;
+    for (int i = tid; i < groups[0] * quads; i += kDecodeThreads) {
+        const int gr = i / quads, e = i - gr * quads;
+        const int x = groups[1 + gr], end = gr + 1 < groups[0] ? groups[2 + gr] : 2 * W;
+        const int hd = e / (D / 4), d = (e - hd * (D / 4)) * 4;
+        const int unit = part_info[part_at(x)].unit, begins = part_info[part_at(x)].begins;
+        int from = -1;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        float Ls = 0.f, M = PKV_NEG_INF;
+        for (int z = x; z < end; ++z) {
+            const int pi = part_at(z);
+            if (part_info[pi].unit < 0) continue;
+            from = part_info[pi].from;
+            const float f = factor[z * GP + hd];
+            const float4 v = *reinterpret_cast<const float4 *>(
+                pi < W ? cut + ((size_t)pi * p.g + hd) * D + d : ends + (pi - W) * (L::kPart / 4) + hd * L::kStride + d);
+            O.x = fmaf(v.x, f, O.x); O.y = fmaf(v.y, f, O.y); O.z = fmaf(v.z, f, O.z); O.w = fmaf(v.w, f, O.w);
+            Ls = fmaf(mL[pi * GP + hd], f, Ls);
+            M = fmaxf(M, mM[pi * GP + hd]);
         }
-        if (!begins) { meta.x = unit; meta.y = done; }
-        else if (!done) meta.z = unit;
-        x = y;
+        if (begins && from >= 0) {
+            const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+            *reinterpret_cast<uint2 *>(p.out + (size_t)unit * p.g * D + hd * D + d) =
+                make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+        } else {
+            // record 1: the unit begins here; 0: it began before
+            const size_t r = ((size_t)blockIdx.x * 2 + begins) * p.g + hd;
+            *reinterpret_cast<float4 *>(p.rec_acc + r * D + d) = O;
+            if (d == 0) p.rec_ml[r] = make_float2(M, Ls);
+            if (e == 0 && from >= 0) p.meta[blockIdx.x] = make_int2(unit, from);
+        }
     }
-    if (tid == 0) p.meta[blockIdx.x] = meta;
 }
 
 // --------------------------------------------------------------- reduce ----
-// Where a unit begins in CTA c of the attention kernel and goes on past it,
-// that unit's records, c's second one and the first ones of the CTAs up to the
-// one where it ends, are merged by log-sum-exp.  Every CTA here looks through
-// the CTAs' notes and lists those units; the (unit, head) rows are dealt out to
-// the warps of the grid, or, of units with many records, to its CTAs.
-constexpr int kMergeWarps = 8;
+// Where a unit ends in CTA c of the attention kernel and began in an earlier
+// one, that unit's records, that CTA's second one and the first ones of the
+// CTAs behind it, are merged by log-sum-exp.  Every CTA here lists those units
+// from the CTAs' notes; the (unit, head) rows are dealt out to the warps of the
+// grid, or, of units with many records, to its CTAs.
+constexpr int kMergeWarps = 16;
 constexpr int kMergeMany = 16;  // records from which a whole CTA takes a row
 constexpr int kMergeMaxCtas = 1184;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const StreamParams p, int ctas) {
     constexpr int EPL = D / 32;
-    __shared__ int s_meta[kMergeMaxCtas][3];  // (unit of record 0, ends, unit of record 1)
-    __shared__ int2 s_few[kMergeMaxCtas], s_many[kMergeMaxCtas];  // (first CTA, records)
+    struct Row { int unit, first, n; };  // a unit, the CTA in which it began, its records
+    __shared__ Row s_few[kMergeMaxCtas], s_many[kMergeMaxCtas];
     __shared__ int s_warp[2][kMergeWarps];
     __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps], s_m[kMergeWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
-    for (int i = tid; i < ctas; i += kMergeWarps * 32) {
-        const int4 m = p.meta[i];
-        s_meta[i][0] = m.x; s_meta[i][1] = m.y; s_meta[i][2] = m.z;
-    }
-    __syncthreads();
     // in the line's order, which every CTA finds alike
     int few = 0, many = 0;
     for (int c0 = 0; c0 < ctas; c0 += kMergeWarps * 32) {
-        const int c = c0 + tid, unit = c < ctas ? s_meta[c][2] : -1;
-        int n = 0;
-        if (unit >= 0) {
-            int e = c + 1;
-            while (e < ctas - 1 && s_meta[e][0] == unit && !s_meta[e][1]) ++e;
-            n = min(e, ctas - 1) - c + 1;
+        const int c = c0 + tid;
+        Row u = {-1, 0, 0};
+        if (c < ctas) {
+            const int2 m = p.meta[c];
+            u.unit = m.x;
+            u.first = m.y;
         }
+        const int n = u.n = u.unit >= 0 ? c - u.first + 1 : 0;
         const bool is_few = n > 0 && n <= kMergeMany, is_many = n > kMergeMany;
         const uint32_t mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, is_many);
         if (lane == 0) { s_warp[0][warp] = __popc(mf); s_warp[1][warp] = __popc(mm); }
@@ -801,22 +856,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const S
             few += s_warp[0][w];
             many += s_warp[1][w];
         }
-        if (is_few) s_few[at_few] = make_int2(c, n);
-        if (is_many) s_many[at_many] = make_int2(c, n);
+        if (is_few) s_few[at_few] = u;
+        if (is_many) s_many[at_many] = u;
         __syncthreads();
     }
     float acc[EPL], lsum, M;
     // records first, first + step, ... of a row
-    auto merge = [&](int2 u, int head, int first, int step) {
-        auto record = [&](int i) { return ((size_t)(u.x + i) * 2 + (i == 0)) * p.g + head; };
+    auto merge = [&](const Row &u, int head, int first, int step) {
+        auto record = [&](int i) { return ((size_t)(u.first + i) * 2 + (i == 0)) * p.g + head; };
         M = PKV_NEG_INF;
-        for (int i = first + step * lane; i < u.y; i += step * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
+        for (int i = first + step * lane; i < u.n; i += step * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
         M = warp_max_f32(M);
         lsum = 0.f;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int i = first; i < u.y; i += step) {
+#pragma unroll 8
+        for (int i = first; i < u.n; i += step) {
             const size_t r = record(i);
             const float2 ml = p.rec_ml[r];
             const float f = ml.x == PKV_NEG_INF ? 0.f : ex2(ml.x - M);
@@ -833,7 +888,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const S
         }
     };
     for (int i = blockIdx.x; i < many * p.g; i += gridDim.x) {
-        const int2 u = s_many[i / p.g];
+        const Row u = s_many[i / p.g];
         const int head = i % p.g;
         merge(u, head, warp, kMergeWarps);
 #pragma unroll
@@ -850,17 +905,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const S
                 Ls = fmaf(s_l[w], f, Ls);
                 O = fmaf(s_o[w][tid], f, O);
             }
-            p.out[((size_t)s_meta[u.x][2] * p.g + head) * D + tid] =
+            p.out[((size_t)u.unit * p.g + head) * D + tid] =
                 __float2bfloat16_rn(Ls > 0.f || Ls != Ls ? O / Ls : 0.f);
         }
         __syncthreads();
     }
     for (int i = blockIdx.x * kMergeWarps + warp; i < few * p.g; i += gridDim.x * kMergeWarps) {
-        const int2 u = s_few[i / p.g];
+        const Row u = s_few[i / p.g];
         const int head = i % p.g;
         merge(u, head, 0, 1);
         const float inv = lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f;
-        __nv_bfloat16 *out = p.out + ((size_t)s_meta[u.x][2] * p.g + head) * D + lane * EPL;
+        __nv_bfloat16 *out = p.out + ((size_t)u.unit * p.g + head) * D + lane * EPL;
 #pragma unroll
         for (int e = 0; e < EPL; e += 2)
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);

@@ -270,20 +270,23 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
 // ------------------------------------------------------- stream decode ----
 
 constexpr int kStreamMaxCtas = pkv::kMergeMaxCtas;  // 8 for each of 148 SMs
-constexpr int kStreamMinStages = 2;  // of a warp, while there are fewer than fill the grid
+constexpr int kStreamMinCost = 4;  // of a warp, while there is less work than fills the grid
+constexpr int kStreamWhole = 16;   // stages of a unit up to which warps take whole units
 constexpr int kStreamRing = 12;      // stages of a CTA in flight (e4m3); 8 of bf16
 
 struct StreamLayout {
     long long ctas;  // as many as can have work, at most kStreamMaxCtas
+    bool whole;      // no unit is cut: nothing to merge
     size_t off_ml, off_acc, off_cut, total;
 };
 
 bool stream_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, long long stages, StreamLayout *w) {
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || stages < 0) return false;
-    const long long line = (long long)B * Hkv * stages;
-    w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * kStreamMinStages), kStreamMaxCtas));
+    const long long line = (long long)B * Hkv * (stages + pkv::kUnitCost);
+    w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * kStreamMinCost), kStreamMaxCtas));
+    w->whole = stages <= kStreamWhole;
     const size_t heads = (size_t)w->ctas * 2 * (Hq / Hkv);
-    w->off_ml = round256((size_t)w->ctas * sizeof(int4));
+    w->off_ml = round256((size_t)w->ctas * sizeof(int2));
     w->off_acc = w->off_ml + round256(heads * sizeof(float2));
     w->off_cut = w->off_acc + round256(heads * D * sizeof(float));
     w->total = w->off_cut + round256(heads / 2 * pkv::kConsumerWarps * D * sizeof(float));
@@ -308,15 +311,16 @@ pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *wo
         if (dev >= 0 && dev < kMaxDevices) occ_cache[dev].store(occ, std::memory_order_release);
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    prm.meta = reinterpret_cast<int4 *>(ws);
+    prm.meta = reinterpret_cast<int2 *>(ws);
     prm.rec_ml = reinterpret_cast<float2 *>(ws + wl.off_ml);
     prm.rec_acc = reinterpret_cast<float *>(ws + wl.off_acc);
     prm.cut = reinterpret_cast<float *>(ws + wl.off_cut);
-    prm.min_stages = kStreamMinStages;
+    prm.min_cost = kStreamMinCost;
+    prm.whole = !SEL && wl.whole;
     const int ctas = (int)std::min<long long>(wl.ctas, (long long)sm_count(dev) * occ);
     ClusterLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, 1, stream);
     if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
-    if (ctas > 1) {
+    if (ctas > 1 && !prm.whole) {
         // a warp for each row that can have been cut, up to two CTAs an SM
         const long long rows = ((long long)ctas * prm.g + pkv::kMergeWarps - 1) / pkv::kMergeWarps;
         ClusterLaunch re(std::min<long long>(rows, 2ll * sm_count(dev)), pkv::kMergeWarps * 32, 0, 1, stream);
