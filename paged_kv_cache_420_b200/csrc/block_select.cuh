@@ -215,19 +215,24 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_blocks_kernel(const Se
 }
 
 // ---------------------------------------------------------- selection ----
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;    // two passes of 11 bits find the K-th score to 22 of its 32
+// A CTA of T threads for each (s, h).  Up to PER scores a thread stay in
+// registers; PER = 0 reads them again (from L2) in each pass.  The search for
+// the K-th score counts keys in 2048 equal bins between the least and the
+// largest (scores of one query lie close together: bins by leading bits would
+// send them all to a few counters), and once more within a bin that is wider
+// than the scores' error.
+constexpr int kSelBins = 2048;
 constexpr int kSelPairMax = 512;  // undecided blocks up to which each is compared with each
 
+template <int T>
 struct SelectSmem {
     uint32_t hist[kSelBins];
     uint64_t key[kSelPairMax];  // undecided blocks, while they are few
     int idx[kSelPairMax];
-    uint32_t scan[kSelWarps];
+    uint32_t scan[T / 32], lo[T / 32], hi[T / 32];
+    float emax[T / 32];
     uint32_t found[2];
     uint32_t undecided;
-    float emax[kSelWarps];
 };
 
 // Order-preserving integers; -0 as +0, NaN as +infinity.
@@ -246,7 +251,8 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 }
 
 // Exclusive prefix sum of a value of each thread, and the total (all threads).
-__device__ __forceinline__ uint32_t block_scan(SelectSmem *sm, uint32_t x, uint32_t &total) {
+template <int T>
+__device__ __forceinline__ uint32_t block_scan(SelectSmem<T> *sm, uint32_t x, uint32_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t incl = x;
 #pragma unroll
@@ -257,39 +263,37 @@ __device__ __forceinline__ uint32_t block_scan(SelectSmem *sm, uint32_t x, uint3
     __syncthreads();  // scan[] is free
     if (lane == 31) sm->scan[warp] = incl;
     __syncthreads();
-    uint32_t w = lane < kSelWarps ? sm->scan[lane] : 0;
+    uint32_t w = lane < T / 32 ? sm->scan[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < kSelWarps; o <<= 1) {
+    for (int o = 1; o < T / 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
-    total = __shfl_sync(0xffffffffu, w, kSelWarps - 1);
+    total = __shfl_sync(0xffffffffu, w, T / 32 - 1);
     const uint32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     return incl - x + (warp > 0 ? before : 0);
 }
 
 // The bin of the histogram that holds the m-th largest key (m >= 1, at most
 // the number of keys) and the number of keys in the bins above it.
-template <int BINS>
-__device__ __forceinline__ void find_bin(SelectSmem *sm, uint32_t m, uint32_t &bin, uint32_t &above) {
-    constexpr int PER = BINS >= kSelThreads ? BINS / kSelThreads : 1;  // bins of a thread, from the top
+template <int BINS, int T>
+__device__ __forceinline__ void find_bin(SelectSmem<T> *sm, uint32_t m, uint32_t &bin, uint32_t &above) {
+    constexpr int PER = BINS >= T ? BINS / T : 1;  // bins of a thread, from the top
     const int b0 = BINS - 1 - (int)threadIdx.x * PER;
-    uint32_t c[PER], sum = 0, total;
+    uint32_t sum = 0, total;
     __syncthreads();  // the histogram is complete
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        c[i] = b0 - i >= 0 ? sm->hist[b0 - i] : 0;
-        sum += c[i];
-    }
-    uint32_t a = block_scan(sm, sum, total);
+    for (int i = 0; i < PER; ++i) sum += b0 - i >= 0 ? sm->hist[b0 - i] : 0;
+    uint32_t a = block_scan<T>(sm, sum, total);
     if (a < m && a + sum >= m) {
-#pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (a < m && a + c[i] >= m) {
+            const uint32_t c = sm->hist[b0 - i];
+            if (a + c >= m) {
                 sm->found[0] = (uint32_t)(b0 - i);
                 sm->found[1] = a;
+                break;
             }
-            a += c[i];
+            a += c;
         }
     }
     __syncthreads();
@@ -297,72 +301,158 @@ __device__ __forceinline__ void find_bin(SelectSmem *sm, uint32_t m, uint32_t &b
     above = sm->found[1];
 }
 
+// A block's score in fp64, as an ordered key.  Eight lanes take a head, each D /
+// 8 of its elements; all lanes return the key.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectParams p) {
-    constexpr int VE = 2 * D;
+__device__ __forceinline__ uint64_t exact_key(const SelectParams &p, const __nv_bfloat16 *q, int blk, int h) {
+    constexpr int E = D / 8;
+    const double inf = __longlong_as_double(0x7ff0000000000000ll);
+    if (blk < 0 || blk >= p.NB) return order_key(-inf);
+    const int lane = threadIdx.x & 31, d0 = (lane & 7) * E;
+    auto load = [&](const __nv_bfloat16 *src, float (&x)[E]) {
+#pragma unroll
+        for (int i = 0; i < E; i += 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + d0 + i));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[i + 2 * c] = bf16lo_to_f32(w[c]);
+                x[i + 2 * c + 1] = bf16hi_to_f32(w[c]);
+            }
+        }
+    };
+    const __nv_bfloat16 *b = p.bounds + ((size_t)blk * p.H + h) * 2 * D;
+    float lo[E], hi[E];
+    load(b, lo);
+    load(b + D, hi);
+    double best = -inf;
+    bool nan = false;
+    for (int j0 = 0; j0 < p.g; j0 += 4) {
+        const int j = j0 + (lane >> 3);
+        double sum[2] = {0.0, 0.0};
+        if (j < p.g) {
+            float x[E];
+            load(q + (size_t)j * D, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const double y = (double)x[i] * (double)lo[i], z = (double)x[i] * (double)hi[i];
+                sum[i & 1] += (y != y || z != z) ? y + z : (y > z ? y : z);
+            }
+        }
+        double t = sum[0] + sum[1];
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (j < p.g) {
+            nan |= t != t;
+            best = t > best ? t : best;
+        }
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        const double t = __shfl_xor_sync(0xffffffffu, best, o);
+        best = t > best ? t : best;
+    }
+    return order_key(__any_sync(0xffffffffu, nan) ? inf : best);
+}
+
+template <int D, int T, int PER>
+__global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) {
+    constexpr int WARPS = T / 32;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    SelectSmem *sm = reinterpret_cast<SelectSmem *>(smem_raw);
+    SelectSmem<T> *sm = reinterpret_cast<SelectSmem<T> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t unit = blockIdx.x;
     const int s = (int)(unit / p.H), h = (int)(unit % p.H);
-    for (int i = tid; i < kSelBins; i += kSelThreads) sm->hist[i] = 0;
+    for (int i = tid; i < kSelBins; i += T) sm->hist[i] = 0;
     if (tid == 0) sm->undecided = 0;
     grid_dependency_wait();
     const int n = select_blocks_of(p, s, h == 0 && tid == 0);
     int32_t *out = p.selected + unit * p.K;
     if (n <= p.K) {
-        for (int i = tid; i < p.K; i += kSelThreads) out[i] = i < n ? i : -1;
+        for (int i = tid; i < p.K; i += T) out[i] = i < n ? i : -1;
         return;
     }
     // a bit for each block: kept, and undecided
     const int words = (n + 31) / 32;
-    uint32_t *kept = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectSmem)), *open = kept + words;
+    uint32_t *kept = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectSmem<T>)), *open = kept + words;
     const float *score = p.scores + unit * p.stride;
     const int32_t *table = p.block_tables + (size_t)s * p.MBS;
     const float inf = __int_as_float(0x7f800000);
-    float e = 0.f;
-    for (int i = tid; i < (n + p.run - 1) / p.run; i += kSelThreads) e = fmaxf(e, p.errors[unit * p.runs + i]);
-    e = warp_max_f32(e);
-    if (lane == 0) sm->emax[warp] = e;
-    __syncthreads();
-    for (int w = 0; w < kSelWarps; ++w) e = fmaxf(e, sm->emax[w]);
-
-    // The K-th largest of the blocks between the first and the last, to 22
-    // bits: it lies in t_lo .. t_hi.
-    const uint32_t want = (uint32_t)(p.K - 2);
+    // Thread t's scores are blocks t, t + T, ...
+    float a[PER > 0 ? PER : 1];
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) a[i] = tid + i * T < n ? score[tid + i * T] : 0.f;
+    }
+    auto each = [&](auto &&f) {  // f(block, score), all threads of a warp together
+        if constexpr (PER > 0) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (warp * 32 + i * T < n) f(tid + i * T, a[i]);
+        } else {
+#pragma unroll 4
+            for (int i = tid; i - lane < n; i += T) f(i, i < n ? score[i] : 0.f);
+        }
+    };
     auto ranked = [&](int i) { return i > 0 && i < n - 1; };
+    float e = 0.f;
+    for (int i = tid; i < (n + p.run - 1) / p.run; i += T) e = fmaxf(e, p.errors[unit * p.runs + i]);
+    uint32_t lo = 0xffffffffu, hi = 0;
+    each([&](int i, float x) {
+        if (ranked(i)) {
+            const uint32_t k = order_key(x);
+            lo = min(lo, k);
+            hi = max(hi, k);
+        }
+    });
+    e = warp_max_f32(e);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) { sm->emax[warp] = e; sm->lo[warp] = lo; sm->hi[warp] = hi; }
+    __syncthreads();
+    for (int w = 0; w < WARPS; ++w) {
+        e = fmaxf(e, sm->emax[w]);
+        lo = min(lo, sm->lo[w]);
+        hi = max(hi, sm->hi[w]);
+    }
+
+    // The K-th largest of the blocks between the first and the last lies in
+    // t_lo .. t_hi.
+    const uint32_t want = (uint32_t)(p.K - 2);
     float t_lo = -inf, t_hi = inf;
     if (want > 0 && e < inf) {
-        uint32_t k0, k1, above, above1;
-        for (int i = tid; i < n; i += kSelThreads)
-            if (ranked(i)) atomicAdd(&sm->hist[order_key(score[i]) >> 21], 1u);
-        find_bin<kSelBins>(sm, want, k0, above);
-        for (int i = tid; i < kSelBins; i += kSelThreads) sm->hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
-            const uint32_t k = order_key(score[i]);
-            if (ranked(i) && (k >> 21) == k0) atomicAdd(&sm->hist[(k >> 10) & (kSelBins - 1)], 1u);
+        uint32_t left = want, base = lo, width = hi - lo;  // the keys base .. base + width
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = max(0, 32 - __clz(width) - 11);
+            each([&](int i, float x) {
+                const uint32_t k = order_key(x) - base;
+                if (ranked(i) && k <= width) atomicAdd(&sm->hist[k >> shift], 1u);
+            });
+            uint32_t bin, above;
+            find_bin<kSelBins, T>(sm, left, bin, above);
+            left -= above;
+            base += bin << shift;
+            width = min(width - (bin << shift), (1u << shift) - 1);
+            t_lo = order_value(base);
+            t_hi = order_value(base + width);
+            if (t_hi - t_lo <= e || width == 0) break;
+            if (pass < 2) {
+                for (int i = tid; i < kSelBins; i += T) sm->hist[i] = 0;
+                __syncthreads();
+            }
         }
-        find_bin<kSelBins>(sm, want - above, k1, above1);
-        t_lo = order_value((k0 << 21) | (k1 << 10));
-        t_hi = order_value((k0 << 21) | (k1 << 10) | 1023u);
     }
     // In, out or undecided.  With an unbounded error every block is undecided.
     const float in_above = t_hi + 2.f * e, out_below = t_lo - 2.f * e;
     uint32_t n_in = 0;
-    for (int w = warp; w < words; w += kSelWarps) {
-        const int i = w * 32 + lane;
-        bool in = false, maybe = false;
-        if (i < n) {
-            const float a = score[i];
-            in = !ranked(i) || (want > 0 && a > in_above);
-            maybe = !in && want > 0 && !(a < out_below);
-        }
+    each([&](int i, float x) {
+        const bool in = i < n && (!ranked(i) || (want > 0 && x > in_above));
+        const bool maybe = i < n && !in && want > 0 && !(x < out_below);
         const uint32_t mi = __ballot_sync(0xffffffffu, in), mu = __ballot_sync(0xffffffffu, maybe);
         n_in += __popc(mi);
         if (lane == 0) {
-            kept[w] = mi;
-            open[w] = mu;
+            kept[i >> 5] = mi;
+            open[i >> 5] = mu;
         }
         if (mu != 0) {
             uint32_t at = 0;
@@ -370,48 +460,20 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(mu & ((1u << lane) - 1));
             if (maybe && at < (uint32_t)kSelPairMax) sm->idx[at] = i;
         }
-    }
+    });
     uint32_t all_in;
-    block_scan(sm, lane == 0 ? n_in : 0, all_in);
+    block_scan<T>(sm, lane == 0 ? n_in : 0, all_in);
     const uint32_t left = p.K - all_in;  // how many of the undecided are kept
     const uint32_t und = sm->undecided;
-    // a block's score in fp64 (all lanes)
     const __nv_bfloat16 *q = p.q + unit * p.g * D;
-    auto exact_key = [&](int i) -> uint64_t {
-        const int blk = __ldg(table + i);
-        if (blk < 0 || blk >= p.NB) return order_key(-__longlong_as_double(0x7ff0000000000000ll));
-        const __nv_bfloat16 *b = p.bounds + ((size_t)blk * p.H + h) * VE;
-        double lo[D / 32], hi[D / 32], best = -__longlong_as_double(0x7ff0000000000000ll);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            lo[c] = (double)__bfloat162float(b[c * 32 + lane]);
-            hi[c] = (double)__bfloat162float(b[D + c * 32 + lane]);
-        }
-        bool nan = false;
-#pragma unroll 4
-        for (int j = 0; j < p.g; ++j) {
-            double sum = 0.0;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const double x = (double)__bfloat162float(q[(size_t)j * D + c * 32 + lane]);
-                const double y = x * lo[c], z = x * hi[c];
-                sum += (y != y || z != z) ? y + z : (y > z ? y : z);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            nan |= sum != sum;
-            best = sum > best ? sum : best;
-        }
-        return order_key(nan ? __longlong_as_double(0x7ff0000000000000ll) : best);
-    };
     if (und <= (uint32_t)kSelPairMax) {
         // few: each against each, one is kept if fewer than `left` are ahead
-        for (uint32_t u = warp; u < und; u += kSelWarps) {
-            const uint64_t k = exact_key(sm->idx[u]);
+        for (uint32_t u = warp; u < und; u += WARPS) {
+            const uint64_t k = exact_key<D>(p, q, __ldg(table + sm->idx[u]), h);
             if (lane == 0) sm->key[u] = k;
         }
         __syncthreads();
-        for (uint32_t u = warp; u < und; u += kSelWarps) {
+        for (uint32_t u = warp; u < und; u += WARPS) {
             const uint64_t k = sm->key[u];
             const int i = sm->idx[u];
             uint32_t ahead = 0;
@@ -427,36 +489,36 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         // many: the left-th largest key by radix, 8 bits a pass, then as many
         // of the blocks that equal it as are missing, the lowest indexes first
         uint64_t *key = p.keys + unit * p.stride;
-        for (int w = warp; w < words; w += kSelWarps)
+        for (int w = warp; w < words; w += WARPS)
             for (uint32_t m = open[w]; m != 0; m &= m - 1) {
                 const int i = w * 32 + __ffs(m) - 1;
-                const uint64_t k = exact_key(i);
+                const uint64_t k = exact_key<D>(p, q, __ldg(table + i), h);
                 if (lane == 0) key[i] = k;
             }
         uint64_t prefix = 0;
         uint32_t rest = left;  // 1 <= left <= und: all but `und` blocks are in or out
         for (int shift = 56; shift >= 0; shift -= 8) {
             __syncthreads();  // keys written; the last pass's histogram read
-            if (tid < 256) sm->hist[tid] = 0;
+            for (int i = tid; i < 256; i += T) sm->hist[i] = 0;
             __syncthreads();
-            for (int i = tid; i < n; i += kSelThreads)
+            for (int i = tid; i < n; i += T)
                 if ((open[i >> 5] >> (i & 31)) & 1u) {
                     const uint64_t k = key[i];
                     if (shift == 56 || (k >> (shift + 8)) == prefix) atomicAdd(&sm->hist[(k >> shift) & 255u], 1u);
                 }
             uint32_t digit, ab;
-            find_bin<256>(sm, rest, digit, ab);
+            find_bin<256, T>(sm, rest, digit, ab);
             prefix = (prefix << 8) | digit;
             rest -= ab;
         }
         uint32_t seen = 0;  // blocks equal to the border so far
-        for (int base = 0; base < n; base += kSelThreads) {
+        for (int base = 0; base < n; base += T) {
             const int i = base + tid;
             const bool und_i = i < n && ((open[i >> 5] >> (i & 31)) & 1u);
             const uint64_t k = und_i ? key[i] : 0;
             const bool eq = und_i && k == prefix;
             uint32_t total;
-            const uint32_t before = seen + block_scan(sm, eq, total);
+            const uint32_t before = seen + block_scan<T>(sm, eq, total);
             seen += total;
             const uint32_t add = __ballot_sync(0xffffffffu, und_i && (k > prefix || (eq && before < rest)));
             if (lane == 0 && add != 0) kept[i >> 5] |= add;  // the warp's word
@@ -465,10 +527,10 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     }
     // the list, in ascending order
     uint32_t at = 0;
-    for (int base = 0; base < words; base += kSelThreads) {
+    for (int base = 0; base < words; base += T) {
         const int w = base + tid;
         uint32_t m = w < words ? kept[w] : 0, total;
-        uint32_t pos = at + block_scan(sm, __popc(m), total);
+        uint32_t pos = at + block_scan<T>(sm, __popc(m), total);
         at += total;
         for (; m != 0; m &= m - 1, ++pos)
             if (pos < (uint32_t)p.K) out[pos] = w * 32 + __ffs(m) - 1;

@@ -232,12 +232,11 @@ pkv_status dispatch_group(int g, const pkv::DecodeParams &prm, const CUtensorMap
 
 // --------------------------------------------- block-sparse decode ----
 
-// A launch of clusters of `splits` CTAs, allowed to start its prologue while
-// the stream's previous kernel ends.
-struct ClusterLaunch {
+// A launch that may start its prologue while the stream's previous kernel ends.
+struct OverlappedLaunch {
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    ClusterLaunch(long long ctas, int threads, size_t smem, int splits, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    OverlappedLaunch(long long ctas, int threads, size_t smem, cudaStream_t stream) {
         std::memset(&cfg, 0, sizeof cfg);
         std::memset(attr, 0, sizeof attr);
         cfg.gridDim = dim3((unsigned)ctas);
@@ -246,12 +245,8 @@ struct ClusterLaunch {
         cfg.stream = stream;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = (unsigned)splits;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = splits > 1 ? 2 : 1;
+        cfg.numAttrs = 1;
     }
 };
 
@@ -318,12 +313,12 @@ pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *wo
     prm.min_cost = kStreamMinCost;
     prm.whole = !SEL && wl.whole;
     const int ctas = (int)std::min<long long>(wl.ctas, (long long)sm_count(dev) * occ);
-    ClusterLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, 1, stream);
+    OverlappedLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, stream);
     if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
     if (ctas > 1 && !prm.whole) {
         // a warp for each row that can have been cut, up to two CTAs an SM
         const long long rows = ((long long)ctas * prm.g + pkv::kMergeWarps - 1) / pkv::kMergeWarps;
-        ClusterLaunch re(std::min<long long>(rows, 2ll * sm_count(dev)), pkv::kMergeWarps * 32, 0, 1, stream);
+        OverlappedLaunch re(std::min<long long>(rows, 2ll * sm_count(dev)), pkv::kMergeWarps * 32, 0, stream);
         if (cudaLaunchKernelEx(&re.cfg, pkv::stream_reduce_kernel<D>, prm, ctas) != cudaSuccess) return PKV_ECUDA;
     }
     return launch_status();
@@ -362,21 +357,31 @@ bool select_layout(int32_t B, int32_t H, int32_t bs, int32_t max_ctx, int sms, S
     return true;
 }
 
+template <int D, int T, int PER>
+pkv_status launch_selection(const pkv::SelectParams &p, long long units, cudaStream_t stream, int dev) {
+    auto kernel = pkv::select_blocks_kernel<D, T, PER>;
+    static DeviceCache done{};
+    if (!allow_smem(kernel, done, dev)) return PKV_ECUDA;
+    OverlappedLaunch se(units, T, sizeof(pkv::SelectSmem<T>) + (size_t)p.stride / 32 * 8, stream);
+    if (cudaLaunchKernelEx(&se.cfg, kernel, p) != cudaSuccess) return PKV_ECUDA;
+    return launch_status();
+}
+
 template <int D>
 pkv_status launch_select(const pkv::SelectParams &p, long long units, cudaStream_t stream) {
     const int dev = current_device();
-    static DeviceCache done_score{}, done_tall{}, done_select{};
+    static DeviceCache done_score{}, done_tall{};
     const bool tall = p.g > 8;
     auto score = tall ? pkv::score_blocks_kernel<D, true> : pkv::score_blocks_kernel<D, false>;
-    auto select = pkv::select_blocks_kernel<D>;
-    if (!allow_smem(score, tall ? done_tall : done_score, dev) || !allow_smem(select, done_select, dev)) return PKV_ECUDA;
-    const size_t smem = sizeof(pkv::SelectSmem) + (size_t)p.stride / 32 * 8;
-    if (smem > kMaxDynamicSmem || units * p.runs > 0x7fffffffll) return PKV_EUNSUPPORTED;
-    ClusterLaunch sc(units * p.runs, pkv::kScoreWarps * 32, pkv::ScoreSmem<D>::kAlloc, 1, stream);
+    if (!allow_smem(score, tall ? done_tall : done_score, dev)) return PKV_ECUDA;
+    if (units * p.runs > 0x7fffffffll || (size_t)p.stride / 32 * 8 > kMaxDynamicSmem - sizeof(pkv::SelectSmem<512>))
+        return PKV_EUNSUPPORTED;
+    OverlappedLaunch sc(units * p.runs, pkv::kScoreWarps * 32, pkv::ScoreSmem<D>::kAlloc, stream);
     if (cudaLaunchKernelEx(&sc.cfg, score, p) != cudaSuccess) return PKV_ECUDA;
-    ClusterLaunch se(units, pkv::kSelThreads, smem, 1, stream);
-    if (cudaLaunchKernelEx(&se.cfg, select, p) != cudaSuccess) return PKV_ECUDA;
-    return launch_status();
+    // scores in registers up to 8192 blocks; small CTAs where 1024 suffice
+    if (p.stride <= 1024) return launch_selection<D, 128, 8>(p, units, stream, dev);
+    if (p.stride <= 8192) return launch_selection<D, 512, 16>(p, units, stream, dev);
+    return launch_selection<D, 512, 0>(p, units, stream, dev);
 }
 
 // -------------------------------------------------------- prefill ----

@@ -47,13 +47,14 @@ SELECTS = [
     ([0, 1, 16, 33, 64, 65, 1000], 2, 4, 128, 16, 4),
     ([1000, 777, 3000], 3, 1, 64, 16, 2),        # K = 2: the first and the last block only
     ([1000, 777, 3000], 3, 1, 64, 16, 3),
-    ([16 * 130, 16 * 1100 + 5], 1, 8, 128, 16, 33),   # a cluster of CTAs for each head
+    ([16 * 130, 16 * 1100 + 5], 1, 8, 128, 16, 33), 
     ([16 * 2000, 16 * 1999 + 1], 1, 3, 64, 16, 700),
     ([16 * 2000], 1, 16, 128, 16, 128),
     ([48 * 300 + 7, 48 * 10], 2, 11, 64, 48, 16),
     ([128 * 200], 1, 5, 128, 128, 199),          # all but one
     ([1024 * 70, 1024 * 3], 1, 2, 128, 1024, 8),
-    ([300 + 13 * i for i in range(80)], 4, 2, 64, 16, 8),  # more heads than SMs: one CTA each
+    ([300 + 13 * i for i in range(80)], 4, 2, 64, 16, 8),
+    ([16 * 9001 + 3, 16 * 8200, 40], 1, 2, 64, 16, 300),  # more scores than a CTA keeps in registers
 ]
 
 
@@ -63,7 +64,7 @@ def test_select(ctx, H, g, D, bs, K):
     check_select(b, random_bounds(b, sum(ctx)), K)
 
 
-@pytest.mark.parametrize("n,K", [(40, 9), (600, 100), (3000, 1500)])
+@pytest.mark.parametrize("n,K", [(40, 9), (600, 100), (3000, 1500), (8500, 700)])
 def test_select_ties(n, K):
     """Equal scores go to the lower index: all bounds alike (more undecided blocks than are compared one by one),
     a zero query, and a few kinds of blocks repeated over the context."""
@@ -180,12 +181,12 @@ SPARSE = [
     ([0, 1, 15, 16, 17, 100, 1000], 2, 1, 128, 16, 5),
     ([0, 1, 15, 16, 17, 100, 1000], 2, 4, 128, 16, 5),
     ([1000, 1], 1, 1, 64, 16, 64),
-    ([5000, 70, 0], 1, 8, 128, 16, 300),       # a cluster of CTAs for each head
+    ([5000, 70, 0], 1, 8, 128, 16, 300),  
     ([5000, 4999], 1, 3, 64, 16, 301),
     ([3000, 17], 1, 16, 128, 48, 40),
     ([3000, 1030], 2, 11, 64, 1024, 3),
     ([2000, 129], 1, 2, 128, 128, 1),
-    ([200 + 7 * i for i in range(70)], 9, 2, 64, 32, 4),  # one CTA for each head
+    ([200 + 7 * i for i in range(70)], 9, 2, 64, 32, 4),
 ]
 
 
