@@ -333,26 +333,17 @@ pkv_status dispatch_stream(const pkv::StreamParams &prm, const StreamLayout &wl,
 }
 
 // Blocks of a (sequence, kv head) at most, and the parts of the workspace: the
-// scores, the error bounds, and the fp64 keys.
+// scores and the fp64 keys.
 struct SelectLayout {
-    long long blocks, stride, runs;
-    int run;
-    size_t off_errors, off_keys, total;
+    long long stride;
+    size_t off_keys, total;
 };
 
-// Runs of two rounds of copies (fewer prologues), or of one when those are too
-// few to fill the SMs.
-bool select_layout(int32_t B, int32_t H, int32_t bs, int32_t max_ctx, int sms, SelectLayout *w) {
+bool select_layout(int32_t B, int32_t H, int32_t bs, int32_t max_ctx, SelectLayout *w) {
     if (B < 0 || H <= 0 || bs <= 0 || max_ctx < 0) return false;
-    w->blocks = std::max<long long>(1, ((long long)max_ctx + bs - 1) / bs);
-    w->stride = (w->blocks + 31) / 32 * 32;
-    const long long rounds = (w->blocks + pkv::kScoreRound - 1) / pkv::kScoreRound;
-    w->run = pkv::kScoreRound * ((long long)B * H * rounds > 6ll * sms ? 2 : 1);
-    w->runs = (w->blocks + w->run - 1) / w->run;
+    w->stride = std::max<long long>(32, (((long long)max_ctx + bs - 1) / bs + 31) / 32 * 32);
     const size_t units = (size_t)B * H;
-    w->off_errors = round256(units * w->stride * sizeof(float));
-    // (sized for runs of one round, so that it does not depend on the GPU)
-    w->off_keys = w->off_errors + round256(units * rounds * sizeof(float));
+    w->off_keys = round256(units * w->stride * sizeof(float2));
     w->total = w->off_keys + round256(units * w->stride * sizeof(uint64_t));
     return true;
 }
@@ -374,9 +365,13 @@ pkv_status launch_select(const pkv::SelectParams &p, long long units, cudaStream
     const bool tall = p.g > 8;
     auto score = tall ? pkv::score_blocks_kernel<D, true> : pkv::score_blocks_kernel<D, false>;
     if (!allow_smem(score, tall ? done_tall : done_score, dev)) return PKV_ECUDA;
-    if (units * p.runs > 0x7fffffffll || (size_t)p.stride / 32 * 8 > kMaxDynamicSmem - sizeof(pkv::SelectSmem<512>))
+    if (units > 0x7fffffffll || (size_t)p.stride / 32 * 8 > kMaxDynamicSmem - sizeof(pkv::SelectSmem<512>))
         return PKV_EUNSUPPORTED;
-    OverlappedLaunch sc(units * p.runs, pkv::kScoreWarps * 32, pkv::ScoreSmem<D>::kAlloc, stream);
+    // three CTAs an SM, or as many as can have work
+    const long long tiles = units * ((p.stride + 7) / 8);
+    const long long ctas = std::max<long long>(
+        1, std::min<long long>(3ll * sm_count(dev), tiles / (pkv::kScoreMinTiles * pkv::kScoreWarps)));
+    OverlappedLaunch sc(ctas, pkv::kScoreThreads, pkv::ScoreSmem<D>::kAlloc, stream);
     if (cudaLaunchKernelEx(&sc.cfg, score, p) != cudaSuccess) return PKV_ECUDA;
     // scores in registers up to 8192 blocks; small CTAs where 1024 suffice
     if (p.stride <= 1024) return launch_selection<D, 128, 8>(p, units, stream, dev);
@@ -993,7 +988,7 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
 size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
                                   int32_t max_context_len) {
     SelectLayout w;
-    return select_layout(num_seqs, num_kv_heads, block_size, max_context_len, 148, &w) ? w.total : 0;
+    return select_layout(num_seqs, num_kv_heads, block_size, max_context_len, &w) ? w.total : 0;
 }
 
 pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *block_tables,
@@ -1015,8 +1010,7 @@ pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *b
         !aligned(selected, 4) || !aligned(workspace, 256))
         return PKV_EINVAL;
     SelectLayout wl;
-    if (!select_layout(num_seqs, num_kv_heads, pool.block_size, max_context_len, sm_count(current_device()), &wl) ||
-        workspace_bytes < wl.total)
+    if (!select_layout(num_seqs, num_kv_heads, pool.block_size, max_context_len, &wl) || workspace_bytes < wl.total)
         return PKV_EINVAL;
     pkv::SelectParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1032,11 +1026,9 @@ pkv_status pkv_select_blocks(const void *q, const void *bounds, const int32_t *b
     p.K = num_selected;
     p.max_ctx = max_context_len;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.scores = reinterpret_cast<float *>(ws);
-    p.errors = reinterpret_cast<float *>(ws + wl.off_errors);
+    p.scores = reinterpret_cast<float2 *>(ws);
     p.keys = reinterpret_cast<uint64_t *>(ws + wl.off_keys);
-    p.run = wl.run;
-    p.runs = (int)wl.runs;
+    p.B = num_seqs;
     p.stride = (int)wl.stride;
     const long long units = (long long)num_seqs * num_kv_heads;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
