@@ -11,7 +11,9 @@
 // that stretches cut are merged in two steps, within the CTA (whose four
 // stretches are neighbours), then, where a unit goes on over CTAs, through at
 // most two records of each CTA that a second kernel merges.  Where all units
-// are short, the stretches end between units, and there is nothing to merge.
+// are short, the stretches end between units, and there is nothing to merge;
+// where units of equal length (selected blocks) are few, a cluster of CTAs takes
+// each and merges its parts through distributed shared memory.
 //
 //   dense:    unit (s, h) has ceil(context / 16) stages; each CTA adds up the
 //             contexts itself (they are few, and in L2)
@@ -364,6 +366,7 @@ struct TileState {
 // ------------------------------------------------------------------- work ----
 
 constexpr int kUnitCost = 2;     // of a unit, in stages
+constexpr int kStreamMaxSplit = 8;
 constexpr int kStreamGroup = 8;  // stages that a stretch's lanes look up at once
 static_assert(kConsumerWarps * kStreamGroup == 32, "a lane of the producer for each stage of a group");
 
@@ -383,6 +386,7 @@ struct StreamParams {
     int pool_rows;
     int min_cost;    // of a stretch, while there is less work than fills the grid
     int whole;       // stretches end between units
+    int split;       // selected: CTAs of a cluster that take a unit; 0: the line is cut anywhere
     float scale_log2;
 };
 
@@ -431,6 +435,8 @@ struct StreamSmem {
     static constexpr int oScan = oInfo + NS * 16;                       // long long [threads][2]: stages, cost
     static constexpr int oWarpSum = oScan + kDecodeThreads * 16;
     static constexpr int oBounds = oWarpSum + (kW + 1) * 16;            // StreamBound [W + 1]
+    static constexpr int oOwn = kW * kPart;  // split: the CTA's partial, behind the parts in the rings
+    static_assert(oOwn % 16 == 0 && oOwn + GP * (D + 2) * 4 <= NS * kStage, "and the CTA's partial");
     static constexpr int oAbort = oBounds + (kW + 1) * (int)sizeof(StreamBound);
     static constexpr int kBytes = oAbort + 16;
     static_assert(kW * kPart <= NS * kStage, "the parts at the stretches' ends fit into the rings");
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 for (int i = tid; i < vec; i += kDecodeThreads)
                     reinterpret_cast<uint4 *>(p.out)[(size_t)s * vec + i] = make_uint4(0, 0, 0, 0);
     }
-    const int ctas = (int)max(1ll, min((long long)gridDim.x, total.y / (W * p.min_cost)));
+    const int ctas = SEL && p.split ? gridDim.x : (int)max(1ll, min((long long)gridDim.x, total.y / (W * p.min_cost)));
     if ((int)blockIdx.x >= ctas || total.x == 0) {
         if (tid == 0) p.meta[blockIdx.x] = make_int2(-1, 0);
         return;
@@ -552,7 +558,8 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
         const long long y = A + (E - A) * tid / W;
         StreamBound bd;
         if constexpr (SEL) {
-            bd.x = y;
+            const int len_u = p.K * spe, unit = p.split ? blockIdx.x / p.split : 0, part = p.split ? blockIdx.x % p.split : 0;
+            bd.x = p.split ? (long long)unit * len_u + (long long)len_u * (part * W + tid) / (p.split * W) : y;
             bd.seq = 0;
             bd.base = bd.cost_base = 0;
         } else {
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 const long long y0 = SEL ? x - i : cost_base + (long long)h * (len_u + kUnitCost) + kUnitCost;
                 int c = (int)min((long long)ctas - 1, (long long)((double)y0 / (double)total.y * ctas) + 1);
                 while (c > 0 && stretch_begin(total.y, ctas, c) > y0) --c;
-                r.st.last = 8 + c;
+                r.st.last = 8 + (SEL && p.split ? 0 : c);
             }
             int blk = i / spe, off_blk = (i - blk * spe) * kStageTok;  // logical block, token in it
             if constexpr (SEL) {
@@ -742,7 +749,9 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            if (st.last == 1) {
+            if (st.last != 0 && SEL && p.split) {
+                tail = st;
+            } else if (st.last == 1) {
                 state.write_out(p.out + (size_t)st.unit * p.g * D, lane, p.g);
             } else if (st.last == 4 || (st.last != 0 && k == len - 1)) {
                 tail = st;  // the stretch ends with it: it stays in registers
@@ -780,8 +789,64 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
         const float mu = mM[part_at(x) * GP + hd];
         factor[x * GP + hd] = mu == PKV_NEG_INF ? 0.f : ex2(mu - M);
     }
-    if (tid == 0) p.meta[blockIdx.x] = make_int2(-1, 0);
+    if (tid == 0 && !(SEL && p.split)) p.meta[blockIdx.x] = make_int2(-1, 0);
     __syncthreads();
+    if constexpr (SEL) {
+        if (p.split) {
+            // one unit: this CTA's partial, then the cluster's
+            const int quads = p.g * D / 4;
+            float *own = reinterpret_cast<float *>(smem + L::oOwn), *own_ml = own + GP * D;  // [g][D], (m, l) of a head
+            for (int i = tid; i < quads; i += kDecodeThreads) {
+                const int hd = i / (D / 4), d = (i - hd * (D / 4)) * 4;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                float Ls = 0.f, M = PKV_NEG_INF;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if (part_info[W + w].unit < 0) continue;  // an empty stretch
+                    const float f = factor[(2 * w + 1) * GP + hd];
+                    const float4 v = *reinterpret_cast<const float4 *>(ends + w * (L::kPart / 4) + hd * L::kStride + d);
+                    O.x = fmaf(v.x, f, O.x); O.y = fmaf(v.y, f, O.y); O.z = fmaf(v.z, f, O.z); O.w = fmaf(v.w, f, O.w);
+                    Ls = fmaf(mL[(W + w) * GP + hd], f, Ls);
+                    M = fmaxf(M, mM[(W + w) * GP + hd]);
+                }
+                *reinterpret_cast<float4 *>(own + hd * D + d) = O;
+                if (d == 0) { own_ml[2 * hd] = M; own_ml[2 * hd + 1] = Ls; }
+            }
+            if (p.split > 1) {
+                cluster_arrive();
+                cluster_wait();
+            } else {
+                __syncthreads();
+            }
+            const int unit = blockIdx.x / p.split, rank = blockIdx.x % p.split;
+            for (int i = rank * kDecodeThreads + tid; i < quads; i += p.split * kDecodeThreads) {
+                const int hd = i / (D / 4), d = (i - hd * (D / 4)) * 4;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                float Ls = 0.f, M = PKV_NEG_INF, m[kStreamMaxSplit];
+#pragma unroll
+                for (int u = 0; u < kStreamMaxSplit; ++u) {
+                    m[u] = u < p.split ? cluster_ld_f32(cluster_addr(own_ml + 2 * hd, u)) : PKV_NEG_INF;
+                    M = fmaxf(M, m[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < kStreamMaxSplit; ++u) {
+                    if (u >= p.split) break;
+                    const float f = m[u] == PKV_NEG_INF ? 0.f : ex2(m[u] - M);
+                    const float4 v = cluster_ld_f32x4(cluster_addr(own + hd * D + d, u));
+                    O.x = fmaf(v.x, f, O.x); O.y = fmaf(v.y, f, O.y); O.z = fmaf(v.z, f, O.z); O.w = fmaf(v.w, f, O.w);
+                    Ls = fmaf(cluster_ld_f32(cluster_addr(own_ml + 2 * hd + 1, u)), f, Ls);
+                }
+                const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+                *reinterpret_cast<uint2 *>(p.out + (size_t)unit * p.g * D + hd * D + d) =
+                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+            }
+            if (p.split > 1) {  // a CTA's shared memory stays until its peers have read it
+                cluster_arrive();
+                cluster_wait();
+            }
+            return;
+        }
+    }
     const int quads = p.g * D / 4;
     for (int i = tid; i < groups[0] * quads; i += kDecodeThreads) {
         const int gr = i / quads, e = i - gr * quads;
@@ -817,108 +882,56 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
 }
 
 // --------------------------------------------------------------- reduce ----
-// Where a unit ends in CTA c of the attention kernel and began in an earlier
-// one, that unit's records, that CTA's second one and the first ones of the
-// CTAs behind it, are merged by log-sum-exp.  Every CTA here lists those units
-// from the CTAs' notes; the (unit, head) rows are dealt out to the warps of the
-// grid, or, of units with many records, to its CTAs.
-constexpr int kMergeWarps = 16;
-constexpr int kMergeMany = 16;  // records from which a whole CTA takes a row
-constexpr int kMergeMaxCtas = 1184;
-
+// CTA (c, head): where a unit ends in CTA c of the attention kernel and began in
+// an earlier one, that unit's records, that CTA's second one and the first ones
+// of the CTAs behind it, are merged by log-sum-exp.  Warp w takes records w, w +
+// 4, ...; lanes own D / 32 elements.
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) stream_reduce_kernel(const StreamParams p, int ctas) {
+__global__ void __launch_bounds__(kReduceWarps * 32) stream_reduce_kernel(const StreamParams p) {
     constexpr int EPL = D / 32;
-    struct Row { int unit, first, n; };  // a unit, the CTA in which it began, its records
-    __shared__ Row s_few[kMergeMaxCtas], s_many[kMergeMaxCtas];
-    __shared__ int s_warp[2][kMergeWarps];
-    __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps], s_m[kMergeWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ float s_o[kReduceWarps][D], s_l[kReduceWarps], s_m[kReduceWarps];
+    const int c = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
-    // in the line's order, which every CTA finds alike
-    int few = 0, many = 0;
-    for (int c0 = 0; c0 < ctas; c0 += kMergeWarps * 32) {
-        const int c = c0 + tid;
-        Row u = {-1, 0, 0};
-        if (c < ctas) {
-            const int2 m = p.meta[c];
-            u.unit = m.x;
-            u.first = m.y;
-        }
-        const int n = u.n = u.unit >= 0 ? c - u.first + 1 : 0;
-        const bool is_few = n > 0 && n <= kMergeMany, is_many = n > kMergeMany;
-        const uint32_t mf = __ballot_sync(0xffffffffu, is_few), mm = __ballot_sync(0xffffffffu, is_many);
-        if (lane == 0) { s_warp[0][warp] = __popc(mf); s_warp[1][warp] = __popc(mm); }
-        __syncthreads();
-        int at_few = few + __popc(mf & ((1u << lane) - 1)), at_many = many + __popc(mm & ((1u << lane) - 1));
-        for (int w = 0; w < kMergeWarps; ++w) {
-            if (w < warp) { at_few += s_warp[0][w]; at_many += s_warp[1][w]; }
-            few += s_warp[0][w];
-            many += s_warp[1][w];
-        }
-        if (is_few) s_few[at_few] = u;
-        if (is_many) s_many[at_many] = u;
-        __syncthreads();
-    }
-    float acc[EPL], lsum, M;
-    // records first, first + step, ... of a row
-    auto merge = [&](const Row &u, int head, int first, int step) {
-        auto record = [&](int i) { return ((size_t)(u.first + i) * 2 + (i == 0)) * p.g + head; };
-        M = PKV_NEG_INF;
-        for (int i = first + step * lane; i < u.n; i += step * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
-        M = warp_max_f32(M);
-        lsum = 0.f;
+    const int2 meta = p.meta[c];
+    if (meta.x < 0) return;
+    const int n = c - meta.y + 1;  // records
+    auto record = [&](int i) { return ((size_t)(meta.y + i) * 2 + (i == 0)) * p.g + head; };
+    float M = PKV_NEG_INF, acc[EPL], lsum = 0.f;
+    for (int i = warp + kReduceWarps * lane; i < n; i += kReduceWarps * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
+    M = warp_max_f32(M);
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
 #pragma unroll 8
-        for (int i = first; i < u.n; i += step) {
-            const size_t r = record(i);
-            const float2 ml = p.rec_ml[r];
-            const float f = ml.x == PKV_NEG_INF ? 0.f : ex2(ml.x - M);
-            lsum = fmaf(ml.y, f, lsum);
-            const float *a = p.rec_acc + r * D + lane * EPL;
-            if constexpr (EPL == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(a);
-                acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
-                acc[2] = fmaf(x.z, f, acc[2]); acc[3] = fmaf(x.w, f, acc[3]);
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(a);
-                acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
-            }
+    for (int i = warp; i < n; i += kReduceWarps) {
+        const size_t r = record(i);
+        const float2 ml = p.rec_ml[r];
+        const float f = ml.x == PKV_NEG_INF ? 0.f : ex2(ml.x - M);
+        lsum = fmaf(ml.y, f, lsum);
+        const float *a = p.rec_acc + r * D + lane * EPL;
+        if constexpr (EPL == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(a);
+            acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
+            acc[2] = fmaf(x.z, f, acc[2]); acc[3] = fmaf(x.w, f, acc[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(a);
+            acc[0] = fmaf(x.x, f, acc[0]); acc[1] = fmaf(x.y, f, acc[1]);
         }
-    };
-    for (int i = blockIdx.x; i < many * p.g; i += gridDim.x) {
-        const Row u = s_many[i / p.g];
-        const int head = i % p.g;
-        merge(u, head, warp, kMergeWarps);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
-        if (lane == 0) { s_l[warp] = lsum; s_m[warp] = M; }
-        __syncthreads();
-        if (tid < D) {
-            float T = PKV_NEG_INF, Ls = 0.f, O = 0.f;
-#pragma unroll
-            for (int w = 0; w < kMergeWarps; ++w) T = fmaxf(T, s_m[w]);
-#pragma unroll
-            for (int w = 0; w < kMergeWarps; ++w) {
-                const float f = s_m[w] == PKV_NEG_INF ? 0.f : ex2(s_m[w] - T);
-                Ls = fmaf(s_l[w], f, Ls);
-                O = fmaf(s_o[w][tid], f, O);
-            }
-            p.out[((size_t)u.unit * p.g + head) * D + tid] =
-                __float2bfloat16_rn(Ls > 0.f || Ls != Ls ? O / Ls : 0.f);
-        }
-        __syncthreads();
     }
-    for (int i = blockIdx.x * kMergeWarps + warp; i < few * p.g; i += gridDim.x * kMergeWarps) {
-        const Row u = s_few[i / p.g];
-        const int head = i % p.g;
-        merge(u, head, 0, 1);
-        const float inv = lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f;
-        __nv_bfloat16 *out = p.out + ((size_t)u.unit * p.g + head) * D + lane * EPL;
 #pragma unroll
-        for (int e = 0; e < EPL; e += 2)
-            *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
+    if (lane == 0) { s_l[warp] = lsum; s_m[warp] = M; }
+    __syncthreads();
+    if (tid < D) {
+        float T = PKV_NEG_INF, Ls = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kReduceWarps; ++w) T = fmaxf(T, s_m[w]);
+#pragma unroll
+        for (int w = 0; w < kReduceWarps; ++w) {
+            const float f = s_m[w] == PKV_NEG_INF ? 0.f : ex2(s_m[w] - T);
+            Ls = fmaf(s_l[w], f, Ls);
+            O = fmaf(s_o[w][tid], f, O);
+        }
+        p.out[((size_t)meta.x * p.g + head) * D + tid] = __float2bfloat16_rn(Ls > 0.f || Ls != Ls ? O / Ls : 0.f);
     }
 }
 

@@ -232,11 +232,12 @@ pkv_status dispatch_group(int g, const pkv::DecodeParams &prm, const CUtensorMap
 
 // --------------------------------------------- block-sparse decode ----
 
-// A launch that may start its prologue while the stream's previous kernel ends.
+// A launch, of clusters of `cluster` CTAs, that may start its prologue while the
+// stream's previous kernel ends.
 struct OverlappedLaunch {
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    OverlappedLaunch(long long ctas, int threads, size_t smem, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    OverlappedLaunch(long long ctas, int threads, size_t smem, cudaStream_t stream, int cluster = 1) {
         std::memset(&cfg, 0, sizeof cfg);
         std::memset(attr, 0, sizeof attr);
         cfg.gridDim = dim3((unsigned)ctas);
@@ -245,8 +246,12 @@ struct OverlappedLaunch {
         cfg.stream = stream;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
     }
 };
 
@@ -264,8 +269,9 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
 
 // ------------------------------------------------------- stream decode ----
 
-constexpr int kStreamMaxCtas = pkv::kMergeMaxCtas;  // 8 for each of 148 SMs
+constexpr int kStreamMaxCtas = 1184;  // 8 for each of 148 SMs
 constexpr int kStreamMinCost = 4;  // of a warp, while there is less work than fills the grid
+constexpr int kStreamLong = 12;    // stages of a warp from which the line of selected blocks is cut anywhere
 constexpr int kStreamWhole = 16;   // stages of a unit up to which warps take whole units
 constexpr int kStreamRing = 12;      // stages of a CTA in flight (e4m3); 8 of bf16
 
@@ -312,14 +318,29 @@ pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *wo
     prm.cut = reinterpret_cast<float *>(ws + wl.off_cut);
     prm.min_cost = kStreamMinCost;
     prm.whole = !SEL && wl.whole;
-    const int ctas = (int)std::min<long long>(wl.ctas, (long long)sm_count(dev) * occ);
+    const long long slots = (long long)sm_count(dev) * occ;
+    if (SEL) {
+        // Selected blocks: units of one length.  Fewer than kStreamLong stages
+        // a warp: clusters that take a unit each.
+        const long long units = (long long)prm.B * prm.Hkv, stages = (long long)prm.K * (prm.bs / pkv::kStageTok);
+        if (units * stages < kStreamLong * pkv::kConsumerWarps * slots) {
+            int split = 1;
+            while (split < pkv::kStreamMaxSplit && units * split * 2 <= slots && stages >= 2 * split * 2 * pkv::kConsumerWarps)
+                split *= 2;
+            prm.split = split;
+            if (units * split > 0x7fffffffll) return PKV_EUNSUPPORTED;
+            OverlappedLaunch at(units * split, pkv::kDecodeThreads, L::kBytes, stream, split);
+            if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
+            return launch_status();
+        }
+    }
+    const int ctas = (int)std::min<long long>(wl.ctas, slots);
     OverlappedLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, stream);
     if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
     if (ctas > 1 && !prm.whole) {
-        // a warp for each row that can have been cut, up to two CTAs an SM
-        const long long rows = ((long long)ctas * prm.g + pkv::kMergeWarps - 1) / pkv::kMergeWarps;
-        OverlappedLaunch re(std::min<long long>(rows, 2ll * sm_count(dev)), pkv::kMergeWarps * 32, 0, stream);
-        if (cudaLaunchKernelEx(&re.cfg, pkv::stream_reduce_kernel<D>, prm, ctas) != cudaSuccess) return PKV_ECUDA;
+        OverlappedLaunch re(ctas, pkv::kReduceWarps * 32, 0, stream);
+        re.cfg.gridDim.y = (unsigned)prm.g;
+        if (cudaLaunchKernelEx(&re.cfg, pkv::stream_reduce_kernel<D>, prm) != cudaSuccess) return PKV_ECUDA;
     }
     return launch_status();
 }
