@@ -441,55 +441,67 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     _check(st, "paged_attn_decode_fp8")
 
 
-def _need_block_scales(k_scales, v_scales, k_cache):
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _need(t, n, torch.float32)
-        if t.shape != k_cache.shape[:2]:
-            raise ValueError(f"{n} must be [num_blocks, num_kv_heads]")
-
-
-def _need_append(block_tables, context_lens, query_start):
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"), (query_start, "query_start")):
-        _need(t, n, torch.int32)
-    B = context_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.dim() != 1 or query_start.shape != (B + 1,):
-        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B], query_start [B + 1]")
-
-
 _current_device = torch._C._cuda_getDevice
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 
 
-def _launch(what: str, tensors, stream, f, *args) -> None:
-    """Calls f(*args, stream) with the tensors' GPU current (None among them: an absent argument); stream None: that
-    GPU's current stream."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{what}: all tensors must be on one device")
+def _tensors(*specs) -> int:
+    """Checks (tensor, name, dtype) triples, all contiguous and on one GPU, whose index it returns."""
+    index = specs[0][0].get_device()
+    for t, name, dtype in specs:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index or index < 0:
+            _need(t, name, dtype)
+            raise ValueError(f"{name}: all tensors must be on one device")
+    return index
+
+
+def _launch(what: str, index: int, stream, f, *args) -> None:
+    """Calls f(*args, stream) with GPU `index` current; stream None: that GPU's current stream."""
+    if stream is None:
+        raw = _current_raw_stream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     previous = _current_device()
-    if index != previous:
-        torch.cuda.set_device(index)
-    try:
-        if stream is None:
-            raw = _current_raw_stream(index)
-        else:
-            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == previous:
         status = f(*args, raw)
-    finally:
-        if index != previous:
+    else:
+        torch.cuda.set_device(index)
+        try:
+            status = f(*args, raw)
+        finally:
             torch.cuda.set_device(previous)
     if status != PKV_OK:
         raise PkvError(status, what)
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace for one call on `stream` (None: the current one)."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _scratch(workspace: Optional[torch.Tensor], nbytes: int, index: int, stream):
+    """(address, bytes, keeper) of a call's workspace: the caller's, or a new one for `stream` (None: the current
+    one).  The keeper has to live until the call is enqueued."""
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != index:
+            raise ValueError("workspace must be contiguous and on the other tensors' device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    ws = torch.empty(nbytes, dtype=_U8, device=index)
     if stream is not None:  # the allocator may hand the memory on once `stream` is through, not before
         ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
-    return ws
+                         else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index))
+    return ws.data_ptr(), nbytes, ws
+
+
+def _cache_sizes(k_cache):
+    if k_cache.dim() != 4:
+        raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    return k_cache.shape
+
+
+def _need_append(block_tables, context_lens, query_start) -> int:
+    """The sequences of an append."""
+    B = context_lens.numel()
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != B or \
+            query_start.dim() != 1 or query_start.numel() != B + 1:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B], query_start [B + 1]")
+    return B
 
 
 def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -497,49 +509,50 @@ def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Te
                         k_cache: torch.Tensor, v_cache: torch.Tensor, max_new_tokens: int, stream=None) -> None:
     """Appends and quantises: rows query_start[s] .. query_start[s+1] - 1 of k and v become the last positions of
     sequence s (context_lens counts them), as e4m3 codes with a power-of-two scale for each (block, kv head).  A
-    block that already holds rows keeps its scale or grows it, and its older codes are rounded anew."""
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, torch.bfloat16)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.uint8)
-    _need_append(block_tables, context_lens, query_start)
-    _need_block_scales(k_scales, v_scales, k_cache)
+    block that already holds rows keeps its scale or grows it, and then its other codes are rounded anew."""
+    index = _tensors((k, "k", _BF16), (v, "v", _BF16), (block_tables, "block_tables", _I32),
+                     (context_lens, "context_lens", _I32), (query_start, "query_start", _I32),
+                     (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32), (k_cache, "k_cache", _U8),
+                     (v_cache, "v_cache", _U8))
+    B = _need_append(block_tables, context_lens, query_start)
+    shape = nb, h, bs, d = _cache_sizes(k_cache)
     T = k.shape[0]
-    if k.shape != (T, k_cache.shape[1], k_cache.shape[3]) or v.shape != k.shape or v_cache.shape != k_cache.shape:
+    if k.shape != (T, h, d) or v.shape != (T, h, d) or v_cache.shape != shape:
         raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim] and the caches alike")
-    _launch("pkv_write_fp8_block", (k, v, block_tables, context_lens, query_start, k_scales, v_scales, k_cache,
-            v_cache), stream, load_library().pkv_write_fp8_block, k.data_ptr(), v.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), context_lens.shape[0], T,
+    if k_scales.shape != (nb, h) or v_scales.shape != (nb, h):
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    _launch("pkv_write_fp8_block", index, stream, load_library().pkv_write_fp8_block, k.data_ptr(), v.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), B, T,
             int(max_new_tokens), k_scales.data_ptr(), v_scales.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            _pool(k_cache))
+            _Pool(nb, h, bs, d, KV_E4M3))
+
+
+def _scale_rows(k_scales, v_scales):
+    if k_scales.dim() != 2 or v_scales.shape != k_scales.shape:
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    return k_scales.shape
 
 
 def pkv_copy_scales(src_dst_pairs, k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
     """Copies row src -> dst of both scale arrays for every (src, dst) host pair: pkv_copy_blocks' companion."""
-    _need_scale_rows(k_scales, v_scales)
+    index = _tensors((k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32))
+    nb, h = _scale_rows(k_scales, v_scales)
     pairs = np.ascontiguousarray(np.asarray(src_dst_pairs, dtype=np.int32).reshape(-1, 2))
-    _launch("pkv_copy_scales", (k_scales, v_scales), stream, load_library().pkv_copy_scales,
-            pairs.ctypes.data_as(ctypes.c_void_p), pairs.shape[0], _ptr(k_scales), _ptr(v_scales), k_scales.shape[0],
-            k_scales.shape[1])
+    _launch("pkv_copy_scales", index, stream, load_library().pkv_copy_scales, pairs.ctypes.data_as(ctypes.c_void_p),
+            pairs.shape[0], k_scales.data_ptr(), v_scales.data_ptr(), nb, h)
 
 
 def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
                     stream=None) -> None:
     """Copies row src -> dst of both scale arrays for the first num_pairs[0] rows of the device pair list: the
     companion of copy_blocks_dev."""
-    _need(cow_pairs, "cow_pairs", torch.int32)
-    _need(num_pairs, "num_pairs", torch.int32)
-    _need_scale_rows(k_scales, v_scales)
-    _launch("pkv_copy_scales_dev", (k_scales, v_scales, cow_pairs, num_pairs), stream,
-            load_library().pkv_copy_scales_dev, _ptr(cow_pairs), _ptr(num_pairs), cow_pairs.shape[0], _ptr(k_scales),
-            _ptr(v_scales), k_scales.shape[0], k_scales.shape[1])
-
-
-def _need_scale_rows(k_scales, v_scales):
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _need(t, n, torch.float32)
-    if k_scales.dim() != 2 or v_scales.shape != k_scales.shape:
-        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    index = _tensors((cow_pairs, "cow_pairs", _I32), (num_pairs, "num_pairs", _I32), (k_scales, "k_scales", _F32),
+                     (v_scales, "v_scales", _F32))
+    nb, h = _scale_rows(k_scales, v_scales)
+    if cow_pairs.dim() != 2 or cow_pairs.shape[1] != 2 or num_pairs.numel() < 1:
+        raise ValueError("cow_pairs must be [max_pairs, 2], num_pairs [1]")
+    _launch("pkv_copy_scales_dev", index, stream, load_library().pkv_copy_scales_dev, cow_pairs.data_ptr(),
+            num_pairs.data_ptr(), cow_pairs.shape[0], k_scales.data_ptr(), v_scales.data_ptr(), nb, h)
 
 
 def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -548,7 +561,20 @@ def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_hea
                                                             max_context_len)
     if n == 0:
         raise ValueError("invalid sizes for the decode workspace")
-    return int(n)
+    return n
+
+
+def _need_decode(q, out, k_cache, v_cache, block_tables, context_lens, num_kv_heads):
+    """(sequences, query heads, head dim) of a decode step over caches of `num_kv_heads` heads, and the pool's sizes."""
+    shape = _cache_sizes(k_cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, num_q_heads, head_dim]")
+    sizes = B, _, D = q.shape
+    if out.shape != sizes or v_cache.shape != shape or shape[3] != D or shape[1] != num_kv_heads:
+        raise ValueError("out must match q, v_cache must match k_cache, and their head dimensions and heads agree")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.dim() != 1 or context_lens.numel() != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    return sizes, shape
 
 
 def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
@@ -556,25 +582,19 @@ def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 scale: float, num_kv_heads: int, out: torch.Tensor, max_context_len: int,
                                 workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_attn_decode over an FP8 (e4m3) pool with a K and a V scale for each (block, kv head)."""
-    for t, n in ((q, "q"), (out, "out")):
-        _need(t, n, torch.bfloat16)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.uint8)
-    _need(block_tables, "block_tables", torch.int32)
-    _need(context_lens, "context_lens", torch.int32)
-    _need_block_scales(k_scales, v_scales, k_cache)
-    B, Hq, D = q.shape
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or D != k_cache.shape[3]:
-        raise ValueError("out must match q, v_cache must match k_cache, and their head dimensions agree")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
-    if workspace is None:
-        workspace = _scratch(decode_fp8_block_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len), q.device, stream)
-    _launch("paged_attn_decode_fp8_block", (q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-            out, workspace), stream, load_library().paged_attn_decode_fp8_block, q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), int(num_kv_heads), out.data_ptr(),
-            _pool(k_cache), int(max_context_len), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    index = _tensors((q, "q", _BF16), (out, "out", _BF16), (k_cache, "k_cache", _U8), (v_cache, "v_cache", _U8),
+                     (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32), (block_tables, "block_tables", _I32),
+                     (context_lens, "context_lens", _I32))
+    (B, Hq, D), (nb, h, bs, d) = _need_decode(q, out, k_cache, v_cache, block_tables, context_lens, num_kv_heads)
+    if k_scales.shape != (nb, h) or v_scales.shape != (nb, h):
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    max_context_len = int(max_context_len)
+    need = 0 if workspace is not None else decode_fp8_block_workspace_bytes(B, Hq, h, D, max_context_len)
+    ws, ws_bytes, keep = _scratch(workspace, need, index, stream)
+    _launch("paged_attn_decode_fp8_block", index, stream, load_library().paged_attn_decode_fp8_block, q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), h, out.data_ptr(),
+            _Pool(nb, h, bs, d, KV_E4M3), max_context_len, ws, ws_bytes)
 
 
 def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -583,37 +603,29 @@ def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_le
     """bounds[b][h][0 / 1] = the least / largest key element of each column over the rows that block b holds, for
     the blocks that an append (query_start as in pkv_write_fp8_block) touches; bounds is bf16 [num_blocks,
     num_kv_heads, 2, head_dim].  k_scales: the block scales of an e4m3 pool, None for a bf16 one."""
-    _need_cache(k_cache, "k_cache")
-    _need_append(block_tables, context_lens, query_start)
-    _need(bounds, "bounds", torch.bfloat16)
-    if bounds.shape != (k_cache.shape[0], k_cache.shape[1], 2, k_cache.shape[3]):
-        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
-    if (k_scales is not None) != (k_cache.dtype == torch.uint8):
+    fp8 = k_cache.dtype is _U8
+    if (k_scales is not None) != fp8:
         raise ValueError("k_scales belong to an e4m3 pool, and only there")
-    if k_scales is not None:
-        _need_block_scales(k_scales, k_scales, k_cache)
-    _launch("pkv_key_bounds", (k_cache, block_tables, context_lens, query_start, bounds, k_scales), stream,
-            load_library().pkv_key_bounds, k_cache.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(),
-            context_lens.shape[0], int(max_new_tokens), bounds.data_ptr(), _pool(k_cache))
-
-
-def _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads):
-    _need(q, "q", torch.bfloat16)
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"), (selected, "selected")):
-        _need(t, n, torch.int32)
-    B = q.shape[0]
-    if q.dim() != 3 or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("q must be [B, num_q_heads, head_dim], block_tables [B, max_blocks_per_seq], context_lens [B]")
-    if selected.dim() != 3 or selected.shape[:2] != (B, num_kv_heads):
-        raise ValueError("selected must be [B, num_kv_heads, num_selected]")
+    specs = ((k_cache, "k_cache", _U8 if fp8 else _BF16), (block_tables, "block_tables", _I32),
+             (context_lens, "context_lens", _I32), (query_start, "query_start", _I32), (bounds, "bounds", _BF16))
+    index = _tensors(*specs, (k_scales, "k_scales", _F32)) if fp8 else _tensors(*specs)
+    B = _need_append(block_tables, context_lens, query_start)
+    nb, h, bs, d = _cache_sizes(k_cache)
+    if bounds.shape != (nb, h, 2, d):
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    if fp8 and k_scales.shape != (nb, h):
+        raise ValueError("k_scales must be [num_blocks, num_kv_heads]")
+    _launch("pkv_key_bounds", index, stream, load_library().pkv_key_bounds, k_cache.data_ptr(),
+            k_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), query_start.data_ptr(), B, int(max_new_tokens), bounds.data_ptr(),
+            _Pool(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16))
 
 
 def select_workspace_bytes(num_seqs: int, num_kv_heads: int, block_size: int, max_context_len: int) -> int:
     n = load_library().pkv_select_workspace_bytes(num_seqs, num_kv_heads, block_size, max_context_len)
     if n == 0:
         raise ValueError("invalid sizes for the selection workspace")
-    return int(n)
+    return n
 
 
 def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -622,19 +634,24 @@ def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch
     """selected[s][h] (int32 [B, num_kv_heads, K], K >= 2) := the logical blocks that decode attention of sequence s
     and kv head h keeps: the first, the last, and the best others by the upper bound of q.k that bounds
     (pkv_key_bounds) give, ascending; a context of at most K blocks keeps all, and -1 fills the row."""
-    _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads)
-    _need(bounds, "bounds", torch.bfloat16)
-    if bounds.dim() != 4 or bounds.shape[1:] != (num_kv_heads, 2, q.shape[2]):
-        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
-    pool = _Pool(bounds.shape[0], bounds.shape[1], int(block_size), bounds.shape[3], KV_BF16)
-    if workspace is None:
-        workspace = _scratch(select_workspace_bytes(q.shape[0], num_kv_heads, block_size, max_context_len), q.device,
-                             stream)
-    _launch("pkv_select_blocks", (q, bounds, block_tables, context_lens, selected, workspace), stream,
-            load_library().pkv_select_blocks, q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), q.shape[0], q.shape[1], int(num_kv_heads), pool,
-            selected.data_ptr(), selected.shape[2], int(max_context_len), workspace.data_ptr(), workspace.numel() *
-            workspace.element_size())
+    index = _tensors((q, "q", _BF16), (bounds, "bounds", _BF16), (block_tables, "block_tables", _I32),
+                     (context_lens, "context_lens", _I32), (selected, "selected", _I32))
+    if q.dim() != 3 or bounds.dim() != 4 or selected.dim() != 3:
+        raise ValueError("q must be [B, num_q_heads, head_dim], bounds [num_blocks, num_kv_heads, 2, head_dim] and "
+                         "selected [B, num_kv_heads, num_selected]")
+    B, Hq, D = q.shape
+    nb, h, two, d = bounds.shape
+    sb, sh, K = selected.shape
+    if h != num_kv_heads or two != 2 or d != D or sb != B or sh != h:
+        raise ValueError("q, bounds and selected must agree in sequences, kv heads and head dimension")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.dim() != 1 or context_lens.numel() != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    max_context_len, bs = int(max_context_len), int(block_size)
+    need = 0 if workspace is not None else select_workspace_bytes(B, h, bs, max_context_len)
+    ws, ws_bytes, keep = _scratch(workspace, need, index, stream)
+    _launch("pkv_select_blocks", index, stream, load_library().pkv_select_blocks, q.data_ptr(), bounds.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, h,
+            _Pool(nb, h, bs, d, KV_BF16), selected.data_ptr(), K, max_context_len, ws, ws_bytes)
 
 
 def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
@@ -643,7 +660,7 @@ def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads:
                                                          num_selected)
     if n == 0:
         raise ValueError("invalid sizes for the decode workspace")
-    return int(n)
+    return n
 
 
 def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -653,29 +670,26 @@ def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
                              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_attn_decode over the rows of the logical blocks selected[s][h] (negative entries: none) that lie under
     the context.  A bf16 pool, or an e4m3 pool with its block scales."""
-    _need_decode_shapes(q, block_tables, context_lens, selected, num_kv_heads)
-    _need(out, "out", torch.bfloat16)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need_cache(t, n)
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("out must match q, v_cache must match k_cache, and their head dimensions agree")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must have the same element type")
-    fp8 = k_cache.dtype == torch.uint8
+    fp8 = k_cache.dtype is _U8
     if (k_scales is not None) != fp8 or (v_scales is not None) != fp8:
         raise ValueError("k_scales and v_scales belong to an e4m3 pool, and only there")
-    if fp8:
-        _need_block_scales(k_scales, v_scales, k_cache)
-    B, Hq, D = q.shape
-    if workspace is None:
-        workspace = _scratch(decode_sparse_workspace_bytes(B, Hq, num_kv_heads, D, k_cache.shape[2], selected.shape[2]),
-                             q.device, stream)
-    _launch("paged_attn_decode_sparse", (q, k_cache, v_cache, block_tables, context_lens, selected, out, k_scales,
-            v_scales, workspace), stream, load_library().paged_attn_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None, v_scales.data_ptr() if fp8 else None,
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), selected.data_ptr(),
-            selected.shape[2], B, Hq, float(scale), int(num_kv_heads), out.data_ptr(), _pool(k_cache),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    cache = _U8 if fp8 else _BF16
+    specs = ((q, "q", _BF16), (out, "out", _BF16), (k_cache, "k_cache", cache), (v_cache, "v_cache", cache),
+             (block_tables, "block_tables", _I32), (context_lens, "context_lens", _I32), (selected, "selected", _I32))
+    index = _tensors(*specs, (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32)) if fp8 else _tensors(*specs)
+    (B, Hq, D), (nb, h, bs, d) = _need_decode(q, out, k_cache, v_cache, block_tables, context_lens, num_kv_heads)
+    if selected.dim() != 3 or selected.shape[0] != B or selected.shape[1] != h:
+        raise ValueError("selected must be [B, num_kv_heads, num_selected]")
+    K = selected.shape[2]
+    if fp8 and (k_scales.shape != (nb, h) or v_scales.shape != (nb, h)):
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    need = 0 if workspace is not None else decode_sparse_workspace_bytes(B, Hq, h, D, bs, K)
+    ws, ws_bytes, keep = _scratch(workspace, need, index, stream)
+    _launch("paged_attn_decode_sparse", index, stream, load_library().paged_attn_decode_sparse, q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
+            v_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), selected.data_ptr(), K, B, Hq, float(scale), h, out.data_ptr(),
+            _Pool(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16), ws, ws_bytes)
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -60,9 +60,13 @@ __device__ __forceinline__ bool touched_block(const TouchParams &p, int s, int i
     return true;
 }
 
-// A warp takes groups of 16 rows, 16 bytes of bf16 a lane: 2 rows at a time
-// at head dim 128, 4 at 64.  A team of W = min(bs / 16, 8) warps shares a
-// unit, one group each up to blocks of 128 tokens.
+// A warp takes groups of rows, 16 bytes of bf16 a lane: 2 rows at a time at
+// head dim 128, 4 at 64, and 16 rows in flight.  A team of W = min(bs / 16, 8)
+// warps shares a unit, one group each up to blocks of 128 tokens.  A unit's
+// chain of loads (query_start and context, table, rows) is 2 us long whatever it
+// moves, so the warps of an SM set the rate: two or four blocks of 16 a warp
+// measured 1.5 us slower than one (8 prompts of up to 2048 tokens, 11.8 against
+// 10.2 us), for their registers halve the warps.
 constexpr int kTouchRows = 16;
 constexpr int kTouchMaxWarps = 8;
 constexpr int kTouchTeams = 4;  // teams of one warp in a CTA
@@ -133,11 +137,13 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     return e4m3x2_from_f32(a.x * ratio, a.y * ratio) | (e4m3x2_from_f32(b.x * ratio, b.y * ratio) << 16);
 }
 
-template <int D>
+// PASSES: rows of a group / rows of a pass (fewer for short appends, whose
+// blocks receive at most that many).
+template <int D, int PASSES>
 __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(const WriteBlockParams p) {
     constexpr int VPR = D / 8;          // lanes of a row
     constexpr int RPP = 32 / VPR;       // rows of a pass
-    constexpr int PASSES = kTouchRows / RPP;
+    constexpr int GROUP = PASSES * RPP;
     __shared__ float s_amax[kTouchMaxWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wt = p.W > 1 ? warp : 0;  // warp of the team; several teams share a CTA only when W is 1
@@ -149,28 +155,26 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
     r /= p.t.H;
     const int i = (int)(r % p.t.J), s = (int)(r / p.t.J);
     TouchedBlock t;
-    if (!touched_block(p.t, s, i, h == 0 && kv == 0 && wt == 0 && lane == 0, &t)) return;
-    const uint4 *x = (kv ? p.v : p.k) + ((size_t)t.token * p.t.H + h) * VPR;
+    if (!touched_block(p.t, s, i, h == 0 && kv == 0 && wt == 0 && lane == 0, &t)) return;  // (the whole team)
     const size_t stride = (size_t)p.t.H * VPR;  // vectors between tokens
+    const int sub = lane / VPR, c = lane % VPR;
+
+    const int fresh = t.held - t.old;  // new rows
+    const uint4 *x = (kv ? p.v : p.k) + ((size_t)t.token * p.t.H + h) * VPR;
     uint2 *cache = (kv ? p.v_cache : p.k_cache) + ((size_t)t.block * p.t.H + h) * p.t.bs * VPR;
     float *scale = (kv ? p.v_scales : p.k_scales) + (size_t)t.block * p.t.H + h;
     const float s_old = t.old > 0 ? *scale : 0.f;
-    const int sub = lane / VPR, c = lane % VPR;
-
     uint4 in[PASSES];
-    auto load = [&](int grp) {
+    auto load = [&](int grp) {  // group `grp` of the new rows
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
-            const int row = grp * kTouchRows + q * RPP + sub;
-            in[q] = row >= t.old && row < t.held ? __ldg(x + (size_t)(row - t.old) * stride + c) : make_uint4(0, 0, 0, 0);
+            const int row = grp * GROUP + q * RPP + sub;
+            in[q] = row < fresh ? __ldg(x + (size_t)row * stride + c) : make_uint4(0, 0, 0, 0);
         }
     };
-    const int g0 = t.old / kTouchRows;  // the first group with new rows
-    int first = wt;
-    while (first < g0) first += p.W;
-    uint32_t m = 0;
     int loaded = -1;
-    for (int grp = first; grp * kTouchRows < t.held; grp += p.W) {
+    uint32_t m = 0;
+    for (int grp = wt; grp * GROUP < fresh; grp += p.W) {
         load(grp);
         loaded = grp;
         uint32_t mg = 0;
@@ -197,9 +201,9 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
         }
         m = max_bf16x2(m, mg);
     }
-    float amax = fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // magnitudes as integers keep their order
+    m = max(m & 0xffffu, m >> 16);
+    float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m) << 16);
     if (p.W > 1) {
         if (lane == 0) s_amax[wt] = amax;
         __syncthreads();
@@ -207,13 +211,13 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
     }
     const float grown = fmaxf(s_old, pow2_scale(amax));
     const float inv = __frcp_rn(grown);  // exact for a power of two
-    for (int grp = first; grp * kTouchRows < t.held; grp += p.W) {
+    for (int grp = wt; grp * GROUP < fresh; grp += p.W) {
         if (grp != loaded) load(grp);
         loaded = grp;
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
-            const int row = grp * kTouchRows + q * RPP + sub;
-            if (row >= t.old && row < t.held) cache[(size_t)row * VPR + c] = codes_from_bf16(in[q], inv);
+            const int row = grp * GROUP + q * RPP + sub;
+            if (row < fresh) cache[(size_t)(t.old + row) * VPR + c] = codes_from_bf16(in[q], inv);
         }
     }
     if (t.old > 0 && grown > s_old) {
@@ -298,6 +302,7 @@ template <int D, bool KV8>
 __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const KeyBoundsParams p) {
     constexpr int VPR = D / 8, RPP = 32 / VPR, PASSES = kTouchRows / RPP;
     constexpr uint32_t kPosInf = KV8 ? 0x7c007c00u : 0x7f807f80u, kNegInf = KV8 ? 0xfc00fc00u : 0xff80ff80u;
+    using Vec = typename std::conditional<KV8, uint2, uint4>::type;
     __shared__ uint4 s_lo[kTouchMaxWarps][VPR], s_hi[kTouchMaxWarps][VPR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wt = p.W > 1 ? warp : 0;
@@ -307,13 +312,13 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
     const long long r = u / p.t.H;
     const int i = (int)(r % p.t.J), s = (int)(r / p.t.J);
     TouchedBlock t;
-    if (!touched_block(p.t, s, i, h == 0 && wt == 0 && lane == 0, &t)) return;
-    const size_t head = (size_t)t.block * p.t.H + h;
+    if (!touched_block(p.t, s, i, h == 0 && wt == 0 && lane == 0, &t)) return;  // (the whole team)
     const int sub = lane / VPR, c = lane % VPR;
+    const size_t head = (size_t)t.block * p.t.H + h;
+    const Vec *x = static_cast<const Vec *>(p.k_cache) + head * p.t.bs * VPR;
+    const float ks = KV8 ? __ldg(p.k_scales + head) : 1.f;
     uint32_t lo[4] = {kPosInf, kPosInf, kPosInf, kPosInf}, hi[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
     for (int grp = wt; grp * kTouchRows < t.held; grp += p.W) {
-        using Vec = typename std::conditional<KV8, uint2, uint4>::type;
-        const Vec *x = static_cast<const Vec *>(p.k_cache) + head * p.t.bs * VPR;
         Vec in[PASSES];
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
@@ -360,7 +365,6 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
         }
     }
     if constexpr (KV8) {
-        const float ks = __ldg(p.k_scales + head);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 l = f32x2_from_f16x2(lo[e]), g = f32x2_from_f16x2(hi[e]);

@@ -366,6 +366,7 @@ struct TileState {
 // ------------------------------------------------------------------- work ----
 
 constexpr int kUnitCost = 2;     // of a unit, in stages
+constexpr int kMinCost = 4;      // of a stretch, while there is less work than fills the grid
 constexpr int kStreamMaxSplit = 8;
 constexpr int kStreamGroup = 8;  // stages that a stretch's lanes look up at once
 static_assert(kConsumerWarps * kStreamGroup == 32, "a lane of the producer for each stage of a group");
@@ -384,7 +385,6 @@ struct StreamParams {
     float *rec_acc;               // workspace: [CTAs][2][g][D]
     int B, Hq, Hkv, g, MBS, bs, NB, K, max_ctx;
     int pool_rows;
-    int min_cost;    // of a stretch, while there is less work than fills the grid
     int whole;       // stretches end between units
     int split;       // selected: CTAs of a cluster that take a unit; 0: the line is cut anywhere
     float scale_log2;
@@ -445,10 +445,23 @@ struct StreamSmem {
 // CTAs of an SM that the registers must allow.
 constexpr int stream_min_ctas(int GPAD, bool KV8) { return GPAD > 8 ? 2 : KV8 ? 4 : 3; }
 
-// Where part i of `parts` of a line of cost `total` begins.
-__device__ __forceinline__ long long stretch_begin(long long total, int parts, int i) {
-    return (total / parts) * i + (total % parts) * i / parts;
+// a / b for a >= 0: a 64-bit division takes hundreds of cycles, and lines are
+// short of 2^32 nearly always.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
+
+// A line of cost `total` in equal parts, the first ones longer by one.
+struct EvenCut {
+    long long q;
+    int r;
+    __device__ __forceinline__ EvenCut(long long total, int parts) : q(quotient(total, parts)), r((int)(total - q * parts)) {}
+    __device__ __forceinline__ long long begin(int i) const { return q * i + min(i, r); }
+    __device__ __forceinline__ int part_of(long long y) const {
+        const long long y1 = (q + 1) * r;
+        return y < y1 ? (int)quotient(y, (int)(q + 1)) : r + (int)quotient(y - y1, (int)q);
+    }
+};
 
 template <int D, int GPAD, int NS, bool KV8, bool SEL>
 __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
@@ -546,15 +559,16 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 for (int i = tid; i < vec; i += kDecodeThreads)
                     reinterpret_cast<uint4 *>(p.out)[(size_t)s * vec + i] = make_uint4(0, 0, 0, 0);
     }
-    const int ctas = SEL && p.split ? gridDim.x : (int)max(1ll, min((long long)gridDim.x, total.y / (W * p.min_cost)));
+    const int ctas = SEL && p.split ? gridDim.x : (int)max(1ll, min((long long)gridDim.x, total.y / (W * kMinCost)));
     if ((int)blockIdx.x >= ctas || total.x == 0) {
         if (tid == 0) p.meta[blockIdx.x] = make_int2(-1, 0);
         return;
     }
+    const EvenCut line(total.y, ctas);
     __syncthreads();
     // The bounds of the warps' stretches: thread t finds the stage at cost y.
     if (tid <= W) {
-        const long long A = stretch_begin(total.y, ctas, blockIdx.x), E = stretch_begin(total.y, ctas, blockIdx.x + 1);
+        const long long A = line.begin(blockIdx.x), E = line.begin(blockIdx.x + 1);
         const long long y = A + (E - A) * tid / W;
         StreamBound bd;
         if constexpr (SEL) {
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 const int nst = stages_of(context(s, false)), cost = nst > 0 ? nst + kUnitCost : 0;
                 const long long off = y - bd.cost_base;
                 if (off < (long long)cost * p.Hkv) {
-                    const int h = (int)(off / cost), in = (int)(off - (long long)h * cost);
+                    const int h = (int)quotient(off, cost), in = (int)(off - (long long)h * cost);
                     const int i = p.whole ? (2 * in > cost ? nst : 0) : max(0, in - kUnitCost);
                     bd.seq = s;
                     bd.x = bd.base + (long long)h * nst + i;
@@ -615,7 +629,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
             int s, h, i, len_u;  // stage i of len_u of unit (s, h)
             if constexpr (SEL) {
                 len_u = p.K * spe;
-                const long long unit = x / len_u;
+                const long long unit = quotient(x, len_u);
                 i = (int)(x - unit * len_u);
                 s = (int)(unit / p.Hkv);
                 h = (int)(unit - (long long)s * p.Hkv);
@@ -629,7 +643,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 s = cs;
                 len_u = nst;
                 const long long off = x - base;
-                h = (int)(off / nst);
+                h = (int)quotient(off, nst);
                 i = (int)(off - (long long)h * nst);
             }
             r.st.unit = s * p.Hkv + h;
@@ -642,9 +656,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
             if (r.st.last == 2 && ends) {
                 // it began in the last CTA whose bound is not behind its first stage
                 const long long y0 = SEL ? x - i : cost_base + (long long)h * (len_u + kUnitCost) + kUnitCost;
-                int c = (int)min((long long)ctas - 1, (long long)((double)y0 / (double)total.y * ctas) + 1);
-                while (c > 0 && stretch_begin(total.y, ctas, c) > y0) --c;
-                r.st.last = 8 + (SEL && p.split ? 0 : c);
+                r.st.last = 8 + (SEL && p.split ? 0 : line.part_of(y0));
             }
             int blk = i / spe, off_blk = (i - blk * spe) * kStageTok;  // logical block, token in it
             if constexpr (SEL) {

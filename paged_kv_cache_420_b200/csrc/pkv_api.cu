@@ -270,10 +270,10 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
 // ------------------------------------------------------- stream decode ----
 
 constexpr int kStreamMaxCtas = 1184;  // 8 for each of 148 SMs
-constexpr int kStreamMinCost = 4;  // of a warp, while there is less work than fills the grid
 constexpr int kStreamLong = 12;    // stages of a warp from which the line of selected blocks is cut anywhere
 constexpr int kStreamWhole = 16;   // stages of a unit up to which warps take whole units
-constexpr int kStreamRing = 12;      // stages of a CTA in flight (e4m3); 8 of bf16
+constexpr int kStreamRing = 48 << 10;      // bytes of a CTA's rings (e4m3: four CTAs an SM)
+constexpr int kStreamRingBf16 = 64 << 10;  // (bf16: three)
 
 struct StreamLayout {
     long long ctas;  // as many as can have work, at most kStreamMaxCtas
@@ -284,7 +284,7 @@ struct StreamLayout {
 bool stream_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, long long stages, StreamLayout *w) {
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || stages < 0) return false;
     const long long line = (long long)B * Hkv * (stages + pkv::kUnitCost);
-    w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * kStreamMinCost), kStreamMaxCtas));
+    w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * pkv::kMinCost), kStreamMaxCtas));
     w->whole = stages <= kStreamWhole;
     const size_t heads = (size_t)w->ctas * 2 * (Hq / Hkv);
     w->off_ml = round256((size_t)w->ctas * sizeof(int2));
@@ -297,7 +297,8 @@ bool stream_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, long long stag
 template <int D, int GPAD, bool KV8, bool SEL>
 pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *workspace, const CUtensorMap &mk,
                          const CUtensorMap &mv, cudaStream_t stream) {
-    constexpr int NS = KV8 ? kStreamRing : 8;
+    // slots of a K and a V tile: 12 or 24 of e4m3, 8 or 16 of bf16 (head dim 128 or 64)
+    constexpr int NS = KV8 ? kStreamRing / (32 * D) : kStreamRingBf16 / (64 * D);
     using L = pkv::StreamSmem<D, GPAD, NS, KV8>;
     auto kernel = pkv::stream_decode_kernel<D, GPAD, NS, KV8, SEL>;
     const int dev = current_device();
@@ -316,7 +317,6 @@ pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *wo
     prm.rec_ml = reinterpret_cast<float2 *>(ws + wl.off_ml);
     prm.rec_acc = reinterpret_cast<float *>(ws + wl.off_acc);
     prm.cut = reinterpret_cast<float *>(ws + wl.off_cut);
-    prm.min_cost = kStreamMinCost;
     prm.whole = !SEL && wl.whole;
     const long long slots = (long long)sm_count(dev) * occ;
     if (SEL) {
@@ -929,13 +929,20 @@ pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *bloc
     p.v_cache = static_cast<uint2 *>(v_cache);
     p.k_scales = k_scales;
     p.v_scales = v_scales;
-    p.units = (long long)num_seqs * p.t.J * p.t.H * 2;
     p.W = touch_warps(pool);
+    p.units = (long long)num_seqs * p.t.J * p.t.H * 2;
     unsigned grid, threads;
     if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (pool.head_dim == 128) pkv::write_fp8_block_kernel<128><<<grid, threads, 0, st>>>(p);
-    else pkv::write_fp8_block_kernel<64><<<grid, threads, 0, st>>>(p);
+    // the rows of a short append (a decode step) fit one pass: fewer registers
+    const int rows = p.t.max_new;
+    if (pool.head_dim == 128) {
+        if (rows <= 2) pkv::write_fp8_block_kernel<128, 1><<<grid, threads, 0, st>>>(p);
+        else pkv::write_fp8_block_kernel<128, 8><<<grid, threads, 0, st>>>(p);
+    } else {
+        if (rows <= 4) pkv::write_fp8_block_kernel<64, 1><<<grid, threads, 0, st>>>(p);
+        else pkv::write_fp8_block_kernel<64, 4><<<grid, threads, 0, st>>>(p);
+    }
     return launch_status();
 }
 
@@ -991,8 +998,8 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
     p.k_cache = k_cache;
     p.k_scales = k_scales;
     p.bounds = static_cast<uint4 *>(bounds);
-    p.units = (long long)num_seqs * p.t.J * p.t.H;
     p.W = touch_warps(pool);
+    p.units = (long long)num_seqs * p.t.J * p.t.H;
     unsigned grid, threads;
     if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
