@@ -15,14 +15,18 @@
 // the few between them are scored again in fp64.
 //
 // Two kernels.  Scoring is bound by the bounds' bytes (512 for a block and
-// head at head dim 128, against 8 D g operations): all tiles of 8 blocks of all
-// sequences and groups of heads form one line, of which every group of warps of
-// the grid takes an equal stretch, a head a warp (the heads of a block lie side
-// by side in memory), through a ring of bulk copies of each warp.  Selection is a CTA for each (s, h)
-// over the scores that the first kernel left in the workspace (in L2).
+// head at head dim 128, against 8 D g operations).  All tiles of 8 blocks of all
+// sequences and groups of 4 heads form one line, of which every CTA takes an
+// equal stretch, a head a warp; a fifth warp looks the blocks up and copies a
+// block's 4 heads, which lie side by side, at once (2 KB: a bulk copy takes its
+// lane 70 cycles to issue, and copies of single heads kept their warps from
+// computing: 64 sequences of 1025 to 8192 tokens, selection included, 25.9 us
+// against 22.0; loads straight into the operand registers 25.6).  Selection is a CTA for each
+// (s, h) over the scores that the first kernel left in the workspace (in L2).
 #pragma once
 
-#include "ptx.cuh"
+#include "decode.cuh"
+#include "even_cut.cuh"
 
 namespace pkv {
 
@@ -54,25 +58,36 @@ __device__ __forceinline__ int select_blocks_of(const SelectParams &p, int s, bo
         if (report) raise_error(PKV_DEVERR_CONTEXT);
         n = n < 0 ? 0 : cap;
     }
-    return (int)(((long long)n + p.bs - 1) / p.bs);
+    return (int)(((uint32_t)n + p.bs - 1) / (uint32_t)p.bs);
 }
 
 // ----------------------------------------------------------- scoring ----
-constexpr int kScoreWarps = 4;
-constexpr int kScoreThreads = kScoreWarps * 32;
-constexpr int kScoreRing = 3;      // tiles of a warp in flight
-constexpr int kScoreMinTiles = 2;  // of a warp, while there are fewer than fill the grid
-constexpr uint64_t kScoreWaitNs = 2000000000ull;
+constexpr int kScoreWarps = 4;  // that compute; one more copies
+constexpr int kScoreThreads = (kScoreWarps + 1) * 32;
+constexpr int kScoreTile = 8;   // blocks of a tile
+constexpr int kScoreRing = 4;   // tiles of a warp in flight
+
+// What the computing warps have to know of a tile.
+struct __align__(16) ScoreTile {
+    int unit;  // (s, first head of the group)
+    int b0;    // its first logical block
+    int good;  // a bit for each block that has a row
+    int none;
+};
 
 template <int D>
 struct ScoreSmem {
-    static constexpr int kBytes = 4 * D;          // a block's bounds
-    static constexpr int kStride = kBytes + 64;   // two blocks' rows of 64 bytes lie in different halves of the banks
-    static constexpr int kWarp = kScoreRing * 8 * kStride;
-    static constexpr int oScan = kScoreWarps * kWarp;              // long long [threads]
-    static constexpr int oSum = oScan + kScoreThreads * 8;         // long long [warps]
-    static constexpr int oBars = oSum + kScoreWarps * 8;
-    static constexpr int kAlloc = oBars + kScoreWarps * kScoreRing * 8;
+    static constexpr int kBytes = 4 * D;  // a block's bounds, of one head
+    // a ring slot of one head's tile at most: the blocks of a tile are `heads`
+    // rows and 64 bytes apart, so that two of them lie in different halves of
+    // the banks
+    static constexpr int kSlot = kScoreTile * (kBytes + 64);
+    static constexpr int oInfo = kScoreWarps * kScoreRing * kSlot;             // ScoreTile [streams][ring]
+    static constexpr int oScan = oInfo + kScoreWarps * kScoreRing * 16;        // long long [threads]
+    static constexpr int oSum = oScan + kScoreThreads * 8;                     // long long [warps]
+    static constexpr int oBars = oSum + (kScoreWarps + 1) * 8;
+    static constexpr int oAbort = oBars + 2 * kScoreWarps * kScoreRing * 8;
+    static constexpr int kAlloc = oAbort + 16;
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -86,25 +101,27 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_blocks_kernel(const Se
     using L = ScoreSmem<D>;
     constexpr int VE = 2 * D;    // elements of a block's bounds
     constexpr int CH = VE / 32;  // 16-byte loads of a lane per block
-    constexpr int R = kScoreRing;
+    constexpr int R = kScoreRing, TB = kScoreTile;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint8_t *ring = smem_raw + warp * L::kWarp;
+    ScoreTile *info = reinterpret_cast<ScoreTile *>(smem_raw + L::oInfo);
     long long *scan = reinterpret_cast<long long *>(smem_raw + L::oScan);
     long long *warp_sum = reinterpret_cast<long long *>(smem_raw + L::oSum);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + L::oBars) + warp * R;
-    if (lane == 0) {
-        for (int t = 0; t < R; ++t) mbar_init(&bars[t], 1);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem_raw + L::oBars), *empty = full + kScoreWarps * R;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + L::oAbort);
+    // groups of 4, 2 or 1 heads: as many warps share a stretch
+    const int heads = p.H % 4 == 0 ? 4 : p.H % 2 == 0 ? 2 : 1, hgroups = p.H / heads, streams = kScoreWarps / heads;
+    if (tid == 0) {
+        for (int i = 0; i < streams * R; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], heads); }
+        *abort_flag = 0;
         fence_mbar_init();
     }
     grid_dependency_wait();
     // The line: sequences with something to choose, their groups of `heads`
     // heads, tiles of 8 blocks.
-    const int heads = p.H % 4 == 0 ? 4 : p.H % 2 == 0 ? 2 : 1, hgroups = p.H / heads;
-    static_assert(kScoreWarps == 4, "a group of 4, 2 or 1 heads");
     auto tiles_of = [&](int s, int &n) {
         n = select_blocks_of(p, s, false);
-        return n > p.K ? (n + 7) / 8 : 0;
+        return n > p.K ? (n + kScoreTile - 1) / kScoreTile : 0;
     };
     const int per = (p.B + kScoreThreads - 1) / kScoreThreads;
     long long sum = 0, total = 0, before = 0;
@@ -118,185 +135,212 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_blocks_kernel(const Se
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    for (int w = 0; w < kScoreWarps; ++w) {
+    for (int w = 0; w <= kScoreWarps; ++w) {
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
     scan[tid] = before + incl - sum;  // the tiles before this thread's sequences
     __syncthreads();
-    const long long parts = max(1ll, min((long long)gridDim.x * (kScoreWarps / heads), total / kScoreMinTiles));
-    const long long me = (long long)blockIdx.x * (kScoreWarps / heads) + warp / heads;
-    if (me >= parts || total == 0) return;
-    const long long a = (total / parts) * me + (total % parts) * me / parts;
-    const int len = (int)((total / parts) * (me + 1) + (total % parts) * (me + 1) / parts - a);
-    if (len == 0) return;
+    const int parts = (int)max(1ll, min((long long)gridDim.x * streams, total));
+    const EvenCut line(total, parts);
+    // Stream j of the CTA: its stretch of the line.
+    auto stretch = [&](int j, long long &a) -> int {
+        const int me = (int)blockIdx.x * streams + j;
+        if (me >= parts || total == 0) return 0;
+        a = line.begin(me);
+        return (int)(line.begin(me + 1) - a);
+    };
 
-    // Lane l looks up block l % 8 of tile 4 G + l / 8 of the stretch.
-    int cs, nt, n;
-    long long base;
-    {
-        int lo = 0, hi = kScoreThreads - 1;  // the last thread whose sequences begin at or before a
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (scan[mid] <= a) lo = mid; else hi = mid - 1;
+    if (warp == kScoreWarps) {
+        // ------------------------------------------------------ producer --
+        // 32 / streams lanes for a stream: they look up as many blocks at once.
+        const int lanes = 32 / streams, j = lane / lanes, sub = lane % lanes, ahead = lanes / TB;  // tiles
+        long long a = 0;
+        const int len = stretch(j, a);
+        int longest = len;
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        int cs = 0, nt = 0, n = 0;
+        long long base = 0;
+        if (len > 0) {
+            int lo = 0, hi = kScoreThreads - 1;  // the last thread whose sequences begin at or before a
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (scan[mid] <= a) lo = mid; else hi = mid - 1;
+            }
+            cs = min(lo * per, p.B - 1);
+            base = scan[lo];
+            nt = tiles_of(cs, n);
         }
-        cs = min(lo * per, p.B - 1);
-        base = scan[lo];
-        nt = tiles_of(cs, n);
+        struct Look {
+            int unit, b, id;  // (s, first head), logical block, physical block as the table has it
+            bool under;       // the context reaches the block
+        };
+        auto look_up = [&](int G) -> Look {  // this lane's block of tile G * ahead + sub / TB
+            const int k = G * ahead + sub / TB;
+            Look r = {-1, 0, -1, false};
+            if (k >= len) return r;
+            const long long x = a + k;
+            while (x >= base + (long long)nt * hgroups) {
+                base += (long long)nt * hgroups;
+                nt = tiles_of(++cs, n);
+            }
+            const uint32_t off = (uint32_t)(x - base);  // below H * blocks / 8, and that below 2^31
+            const int hg = (int)(off / (uint32_t)nt);
+            r.unit = cs * p.H + hg * heads;
+            r.b = (int)(off - (uint32_t)hg * nt) * TB + sub % TB;
+            r.under = r.b < n;
+            if (r.under) r.id = __ldg(p.block_tables + (size_t)cs * p.MBS + r.b);
+            return r;
+        };
+        const int slot_bytes = heads * L::kSlot, row_bytes = heads * L::kBytes;
+        bool ok = true;
+        int issued = 0;
+        Look next = look_up(0);
+        for (int G = 0; G * ahead < longest && ok; ++G) {
+            const Look cur = next;
+            next = look_up(G + 1);
+            const bool have = cur.id >= 0 && cur.id < p.NB;
+            if (cur.under && !have && cur.unit % p.H == 0) raise_error(PKV_DEVERR_BLOCK);
+            const uint32_t good = __ballot_sync(0xffffffffu, have);
+            for (int t = 0; t < ahead && ok; ++t) {
+                const int k = G * ahead + t, slot = j * R + k % R;
+                const bool mine = sub / TB == t && k < len;
+                bool lane_ok = true;
+                if (mine) {
+                    lane_ok = wait_slot(&empty[slot], ((k / R) & 1) ^ 1, abort_flag);
+                    if (lane_ok && sub % TB == 0) {
+                        ScoreTile ti;
+                        ti.unit = cur.unit;
+                        ti.b0 = cur.b;
+                        ti.good = (int)((good >> lane) & ((1u << TB) - 1));
+                        ti.none = 0;
+                        info[slot] = ti;
+                        mbar_arrive_expect_tx(&full[slot], (uint32_t)(__popc(ti.good) * row_bytes));
+                    }
+                }
+                ok = __all_sync(0xffffffffu, lane_ok);
+                if (mine && ok && have)
+                    bulk_load(smem_raw + j * R * slot_bytes + (k % R) * slot_bytes + (sub % TB) * (row_bytes + 64),
+                              p.bounds + ((size_t)cur.id * p.H + cur.unit % p.H) * VE, row_bytes, &full[slot]);
+                if (k < len) issued = k + 1;
+            }
+        }
+        // After a wait that gave up, what is in flight still has to land.
+        if (!ok && sub == 0)
+            for (int k = max(0, issued - R); k < issued; ++k) mbar_wait_bounded(&full[j * R + k % R], (k / R) & 1, kWaitLimitNs);
+        grid_launch_dependents();
+        return;
     }
-    struct Look {
-        int unit, b, row;  // (s, h), logical block, row of its bounds (-1: none)
-    };
-    auto look_up = [&](int G) -> Look {
-        const int k = 4 * G + (lane >> 3);
-        Look r = {-1, 0, -1};
-        if (k >= len) return r;
-        const long long x = a + k;
-        while (x >= base + (long long)nt * hgroups) {
-            base += (long long)nt * hgroups;
-            nt = tiles_of(++cs, n);
-        }
-        const uint32_t off = (uint32_t)(x - base);  // below H * blocks / 8, and that below 2^31
-        const int hg = (int)(off / (uint32_t)nt), h = hg * heads + warp % heads;
-        r.unit = cs * p.H + h;
-        r.b = (int)(off - (uint32_t)hg * nt) * 8 + (lane & 7);
-        if (r.b < n) {
-            const int id = __ldg(p.block_tables + (size_t)cs * p.MBS + r.b);
-            if (id >= 0 && id < p.NB) r.row = id * p.H + h;
-            else if (h == 0) raise_error(PKV_DEVERR_BLOCK);
-        }
-        return r;
-    };
-    // Copies tile k, which the lanes l / 8 = k % 4 of `t` know.
-    auto issue = [&](int k, const Look &t) {
-        const bool mine = (lane >> 3) == (k & 3) && t.row >= 0;
-        const uint32_t who = __ballot_sync(0xffffffffu, mine);
-        const int slot = k % R;
-        if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(who) * L::kBytes);
-        __syncwarp();
-        if (mine)
-            bulk_load(ring + (slot * 8 + (lane & 7)) * L::kStride, p.bounds + (size_t)t.row * VE, L::kBytes, &bars[slot]);
-    };
-    Look cur = look_up(0), next = look_up(1);
-    for (int k = 0; k < min(R, len); ++k) issue(k, cur);
-
+    // -------------------------------------------------------- consumer --
+    const int j = warp / heads, hd = warp % heads;  // its stream, its head of the group
+    long long a = 0;
+    const int len = stretch(j, a);
     // A fragments of the heads' min(q, 0) and max(q, 0): lane (r = lane / 4,
     // j = lane % 4) holds rows r and r + 8.  Chunk i of a block's bounds is its
     // elements 32 i .. 32 i + 31; lane j reads 8 of them, 32 i + 8 j .. + 7,
     // which are the operands of two k-steps (the order of k is free).  The
     // first half of the chunks are least elements, the second largest ones.
+    const float inf = __int_as_float(0x7f800000);
     uint32_t a0[CH][4], a1[TALL ? CH : 1][4];
     float qsum = 0.f;  // the largest sum |q_jd| of a head
     auto load_q = [&](int unit) {
-        auto row = [&](int head, uint32_t (&f)[CH][4]) {
+        float sum[2] = {0.f, 0.f};
+        auto row = [&](int head, uint32_t (&f)[CH][4], float &sum) {
             const __nv_bfloat16 *q = p.q + ((size_t)unit * p.g + head) * D + 8 * (lane & 3);
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
                 const uint4 v = head < p.g ? __ldg(reinterpret_cast<const uint4 *>(q + 32 * i)) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                f[i][0] = v.x; f[i][1] = v.y; f[i][2] = v.z; f[i][3] = v.w;
+            }
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const uint32_t neg = (w[u] & 0x8000u ? 0xffffu : 0u) | (w[u] & 0x80000000u ? 0xffff0000u : 0u);
-                    f[i][u] = w[u] & neg;
-                    f[i + CH / 2][u] = w[u] & ~neg;
+                    const uint32_t w = f[i][u];
+                    sum += fabsf(bf16lo_to_f32(w));
+                    t += fabsf(bf16hi_to_f32(w));
+                    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(f[i][u]) : "r"(w), "r"(0u));
+                    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(f[i + CH / 2][u]) : "r"(w), "r"(0u));
                 }
-            }
+            sum += t;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (sum != sum) sum = inf;
         };
-        row(lane >> 2, a0);
-        if constexpr (TALL) row((lane >> 2) + 8, a1);
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                s0 += fabsf(bf16lo_to_f32(a0[i][u])) + fabsf(bf16hi_to_f32(a0[i][u]));
-                if constexpr (TALL) s1 += fabsf(bf16lo_to_f32(a1[i][u])) + fabsf(bf16hi_to_f32(a1[i][u]));
-            }
-        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-        s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
-        qsum = warp_max_f32(fmaxf(s0, s1));
+        row(lane >> 2, a0, sum[0]);
+        if constexpr (TALL) row((lane >> 2) + 8, a1, sum[1]);
+        qsum = warp_max_f32(fmaxf(sum[0], sum[1]));
     };
-    const float inf = __int_as_float(0x7f800000);
     int unit = -1;
+    const int slot_bytes = heads * L::kSlot, block_stride = heads * L::kBytes + 64;
     for (int k = 0; k < len; ++k) {
-        const int src_lane = 8 * (k & 3);
-        const int u = __shfl_sync(0xffffffffu, cur.unit, src_lane), b0 = __shfl_sync(0xffffffffu, cur.b, src_lane);
-        if (u != unit) {
-            unit = u;
+        const int slot = j * R + k % R;
+        if (!wait_or_abort(&full[slot], (k / R) & 1, abort_flag)) break;
+        const ScoreTile ti = info[slot];
+        if (ti.unit + hd != unit) {
+            unit = ti.unit + hd;
             load_q(unit);
         }
-        const int slot = k % R;
-        bool ok = mbar_wait_bounded(&bars[slot], (k / R) & 1, kScoreWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {  // copies in flight have to land before the warp ends
-            for (int t = k + 1; t < min(len, k + R); ++t) mbar_wait_bounded(&bars[t % R], (t / R) & 1, kScoreWaitNs);
-            return;
-        }
         // (a block without a row leaves old bytes here, and garbage in its own column only)
-        const bool good = __shfl_sync(0xffffffffu, cur.row, src_lane + (lane >> 2)) >= 0;
-        const uint32_t src = smem_u32(ring) + (slot * 8 + (lane >> 2)) * L::kStride + 16 * (lane & 3);
+        const uint32_t src = smem_u32(smem_raw) + slot * slot_bytes + (lane >> 2) * block_stride + hd * L::kBytes + 16 * (lane & 3);
+        const uint32_t good = (uint32_t)ti.good;
         float d[2][4];
         uint32_t w_lo = 0, w_hi = 0;  // the largest least element above 0, the smallest largest one below
 #pragma unroll
         for (int c = 0; c < 4; ++c) d[0][c] = d[1][c] = 0.f;
+        uint4 x[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[c].x), "=r"(x[c].y), "=r"(x[c].z), "=r"(x[c].w)
+                         : "r"(src + 64 * c));
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            uint4 x;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "r"(src + 64 * c));
             float(&e)[4] = d[c & 1];
             const uint32_t z0 = TALL ? a1[TALL ? c : 0][0] : 0u, z1 = TALL ? a1[TALL ? c : 0][1] : 0u;
             const uint32_t z2 = TALL ? a1[TALL ? c : 0][2] : 0u, z3 = TALL ? a1[TALL ? c : 0][3] : 0u;
-            mma_bf16_16816(e[0], e[1], e[2], e[3], a0[c][0], z0, a0[c][1], z1, x.x, x.y);
-            mma_bf16_16816(e[0], e[1], e[2], e[3], a0[c][2], z2, a0[c][3], z3, x.z, x.w);
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+            mma_bf16_16816(e[0], e[1], e[2], e[3], a0[c][0], z0, a0[c][1], z1, x[c].x, x[c].y);
+            mma_bf16_16816(e[0], e[1], e[2], e[3], a0[c][2], z2, a0[c][3], z3, x[c].z, x[c].w);
+            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (c < CH / 2) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w_lo) : "r"(y[u]));
-                else asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w_hi) : "r"(y[u]));
+            for (int i = 0; i < 4; ++i) {
+                if (c < CH / 2) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w_lo) : "r"(v[i]));
+                else asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w_hi) : "r"(v[i]));
             }
         }
         __syncwarp();
-        if (k + R < len) issue(k + R, ((k + R) >> 2) == (k >> 2) ? cur : next);  // the slot is read
+        if (lane == 0) mbar_arrive(&empty[slot]);  // the slot is read
         // w of the tile, as bits: a NaN is above every number
         w_hi &= 0x7fff7fffu;
         uint32_t wb = max(max(w_lo & 0xffffu, w_lo >> 16), max(w_hi & 0xffffu, w_hi >> 16));
-        wb = __reduce_max_sync(0xffffffffu, good ? wb : 0u);
+        wb = __reduce_max_sync(0xffffffffu, (good >> (lane >> 2)) & 1u ? wb : 0u);
         // rows r and r + 8 of columns 2 j and 2 j + 1: the max over the heads,
         // NaN if one is
         const int r = lane >> 2;
-        float s0 = -inf, s1 = -inf;
-        if (r < p.g) {
-            s0 = d[0][0] + d[1][0];
-            s1 = d[0][1] + d[1][1];
-        }
-        if (TALL && r + 8 < p.g) {
-            s0 = max_nan(s0, d[0][2] + d[1][2]);
-            s1 = max_nan(s1, d[0][3] + d[1][3]);
+        float sc[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            sc[c] = r < p.g ? d[0][c] + d[1][c] : -inf;
+            if (TALL && r + 8 < p.g) sc[c] = max_nan(sc[c], d[0][c + 2] + d[1][c + 2]);
         }
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            s0 = max_nan(s0, __shfl_xor_sync(0xffffffffu, s0, o));
-            s1 = max_nan(s1, __shfl_xor_sync(0xffffffffu, s1, o));
-        }
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) sc[c] = max_nan(sc[c], __shfl_xor_sync(0xffffffffu, sc[c], o));
         // Room for products below fp32's normal range.  Where a sum of
         // magnitudes is not finite, or so large that the sums may not be,
         // nothing is known of the score.
         const float neg = 2.f * qsum * __uint_as_float(wb << 16);
-        float e0 = fmaxf(s0, 0.f) + neg, e1 = fmaxf(s1, 0.f) + neg;
-        e0 = e0 < 1e37f && s0 == s0 ? fmaf(e0, kSelError, 1e-33f) : inf;
-        e1 = e1 < 1e37f && s1 == s1 ? fmaf(e1, kSelError, 1e-33f) : inf;
-        const uint32_t bad = __ballot_sync(0xffffffffu, !good);  // of block c: bit 4 c
-        if (lane < 4)
-            *reinterpret_cast<float4 *>(p.scores + (size_t)unit * p.stride + b0 + 2 * lane) =
-                make_float4((bad >> (8 * lane)) & 1u ? -inf : s0, (bad >> (8 * lane)) & 1u ? 0.f : e0,
-                            (bad >> (8 * lane + 4)) & 1u ? -inf : s1, (bad >> (8 * lane + 4)) & 1u ? 0.f : e1);
-        if ((k & 3) == 3) {
-            cur = next;
-            next = look_up((k >> 2) + 2);
+        auto bound = [&](float y) {
+            const float m = fmaxf(y, 0.f) + neg;
+            return m < 1e37f && y == y ? fmaf(m, kSelError, 1e-33f) : inf;
+        };
+        if (lane < 4) {
+            const bool g0 = (good >> (2 * lane)) & 1u, g1 = (good >> (2 * lane + 1)) & 1u;
+            *reinterpret_cast<float4 *>(p.scores + (size_t)unit * p.stride + ti.b0 + 2 * lane) =
+                make_float4(g0 ? sc[0] : -inf, g0 ? bound(sc[0]) : 0.f, g1 ? sc[1] : -inf, g1 ? bound(sc[1]) : 0.f);
         }
     }
     grid_launch_dependents();
@@ -305,17 +349,16 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_blocks_kernel(const Se
 // ---------------------------------------------------------- selection ----
 // A CTA of T threads for each (s, h).  Up to PER scores a thread stay in
 // registers; PER = 0 reads them again (from L2) in each pass.  The search for
-// the K-th score counts keys in 2048 equal bins between the least and the
+// the K-th score counts keys in 4 T equal bins between the least and the
 // largest (scores of one query lie close together: bins by leading bits would
 // send them all to a few counters), and again within a bin that holds more
 // keys than there are warps to score them again, until it is as narrow as the
 // scores' error.
-constexpr int kSelBins = 2048;
 constexpr int kSelPairMax = 512;  // undecided blocks up to which each is compared with each
 
 template <int T>
 struct SelectSmem {
-    uint32_t hist[kSelBins];
+    uint32_t hist[4 * T];
     uint64_t key[kSelPairMax];  // undecided blocks, while they are few
     int idx[kSelPairMax];
     uint32_t scan[T / 32], lo[T / 32], hi[T / 32];
@@ -365,26 +408,23 @@ __device__ __forceinline__ uint32_t block_scan(SelectSmem<T> *sm, uint32_t x, ui
 
 // The bin of the histogram that holds the m-th largest key (m >= 1, at most
 // the number of keys), the number of keys in the bins above it, and in it.
-template <int BINS, int T>
+// Thread t takes bins 4 (T - 1 - t) .. + 3, the topmost first.
+template <int T>
 __device__ __forceinline__ void find_bin(SelectSmem<T> *sm, uint32_t m, uint32_t &bin, uint32_t &above, uint32_t &inside) {
-    constexpr int PER = BINS >= T ? BINS / T : 1;  // bins of a thread, from the top
-    const int b0 = BINS - 1 - (int)threadIdx.x * PER;
-    uint32_t sum = 0, total;
+    const int b0 = 4 * (T - 1 - (int)threadIdx.x);
     __syncthreads();  // the histogram is complete
+    const uint4 v = *reinterpret_cast<const uint4 *>(&sm->hist[b0]);
+    const uint32_t c[4] = {v.w, v.z, v.y, v.x};
+    uint32_t total;
+    uint32_t a = block_scan<T>(sm, v.x + v.y + v.z + v.w, total);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += b0 - i >= 0 ? sm->hist[b0 - i] : 0;
-    uint32_t a = block_scan<T>(sm, sum, total);
-    if (a < m && a + sum >= m) {
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t c = sm->hist[b0 - i];
-            if (a + c >= m) {
-                sm->found[0] = (uint32_t)(b0 - i);
-                sm->found[1] = a;
-                sm->found[2] = c;
-                break;
-            }
-            a += c;
+    for (int i = 0; i < 4; ++i) {
+        if (a < m && a + c[i] >= m) {
+            sm->found[0] = (uint32_t)(b0 + 3 - i);
+            sm->found[1] = a;
+            sm->found[2] = c[i];
         }
+        a += c[i];
     }
     __syncthreads();
     bin = sm->found[0];
@@ -449,12 +489,14 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams &p, const __nv_
 template <int D, int T, int PER>
 __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) {
     constexpr int WARPS = T / 32;
+    constexpr int kBits = T == 512 ? 11 : 9;  // of 4 T bins
+    static_assert(4 * T == 1 << kBits, "bins");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     SelectSmem<T> *sm = reinterpret_cast<SelectSmem<T> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t unit = blockIdx.x;
     const int s = (int)(unit / p.H), h = (int)(unit % p.H);
-    for (int i = tid; i < kSelBins; i += T) sm->hist[i] = 0;
+    *reinterpret_cast<uint4 *>(&sm->hist[4 * tid]) = make_uint4(0, 0, 0, 0);
     if (tid == 0) sm->undecided = 0;
     grid_dependency_wait();
     const int n = select_blocks_of(p, s, h == 0 && tid == 0);
@@ -518,24 +560,22 @@ __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) 
     float t_lo = -inf, t_hi = inf;
     if (want > 0 && e < inf) {
         uint32_t left = want, base = lo, width = hi - lo;  // the keys base .. base + width
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = max(0, 32 - __clz(width) - 11);
+        for (int pass = 0; pass < (31 + kBits) / kBits; ++pass) {
+            const int shift = max(0, 32 - __clz(width) - kBits);
             each([&](int i, float x) {
                 const uint32_t k = order_key(x) - base;
                 if (ranked(i) && k <= width) atomicAdd(&sm->hist[k >> shift], 1u);
             });
             uint32_t bin, above, inside;
-            find_bin<kSelBins, T>(sm, left, bin, above, inside);
+            find_bin<T>(sm, left, bin, above, inside);
             left -= above;
             base += bin << shift;
             width = min(width - (bin << shift), (1u << shift) - 1);
             t_lo = order_value(base);
             t_hi = order_value(base + width);
             if (inside <= WARPS || t_hi - t_lo <= e || width == 0) break;
-            if (pass < 2) {
-                for (int i = tid; i < kSelBins; i += T) sm->hist[i] = 0;
-                __syncthreads();
-            }
+            *reinterpret_cast<uint4 *>(&sm->hist[4 * tid]) = make_uint4(0, 0, 0, 0);
+            __syncthreads();
         }
     }
     // In, out or undecided.  With an unbounded error every block is undecided.
@@ -595,7 +635,7 @@ __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) 
         uint32_t rest = left;  // 1 <= left <= und: all but `und` blocks are in or out
         for (int shift = 56; shift >= 0; shift -= 8) {
             __syncthreads();  // keys written; the last pass's histogram read
-            for (int i = tid; i < 256; i += T) sm->hist[i] = 0;
+            *reinterpret_cast<uint4 *>(&sm->hist[4 * tid]) = make_uint4(0, 0, 0, 0);
             __syncthreads();
             for (int i = tid; i < n; i += T)
                 if ((open[i >> 5] >> (i & 31)) & 1u) {
@@ -603,7 +643,7 @@ __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) 
                     if (shift == 56 || (k >> (shift + 8)) == prefix) atomicAdd(&sm->hist[(k >> shift) & 255u], 1u);
                 }
             uint32_t digit, ab, inside;
-            find_bin<256, T>(sm, rest, digit, ab, inside);
+            find_bin<T>(sm, rest, digit, ab, inside);
             prefix = (prefix << 8) | digit;
             rest -= ab;
         }

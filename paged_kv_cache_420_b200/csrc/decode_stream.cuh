@@ -27,6 +27,7 @@
 #pragma once
 
 #include "decode.cuh"
+#include "even_cut.cuh"
 
 namespace pkv {
 
@@ -444,24 +445,6 @@ struct StreamSmem {
 
 // CTAs of an SM that the registers must allow.
 constexpr int stream_min_ctas(int GPAD, bool KV8) { return GPAD > 8 ? 2 : KV8 ? 4 : 3; }
-
-// a / b for a >= 0: a 64-bit division takes hundreds of cycles, and lines are
-// short of 2^32 nearly always.
-__device__ __forceinline__ long long quotient(long long a, int b) {
-    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
-// A line of cost `total` in equal parts, the first ones longer by one.
-struct EvenCut {
-    long long q;
-    int r;
-    __device__ __forceinline__ EvenCut(long long total, int parts) : q(quotient(total, parts)), r((int)(total - q * parts)) {}
-    __device__ __forceinline__ long long begin(int i) const { return q * i + min(i, r); }
-    __device__ __forceinline__ int part_of(long long y) const {
-        const long long y1 = (q + 1) * r;
-        return y < y1 ? (int)quotient(y, (int)(q + 1)) : r + (int)quotient(y - y1, (int)q);
-    }
-};
 
 template <int D, int GPAD, int NS, bool KV8, bool SEL>
 __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))

@@ -382,16 +382,16 @@ pkv_status launch_selection(const pkv::SelectParams &p, long long units, cudaStr
 template <int D>
 pkv_status launch_select(const pkv::SelectParams &p, long long units, cudaStream_t stream) {
     const int dev = current_device();
-    static DeviceCache done_score{}, done_tall{};
     const bool tall = p.g > 8;
+    static DeviceCache done_score{}, done_tall{};
     auto score = tall ? pkv::score_blocks_kernel<D, true> : pkv::score_blocks_kernel<D, false>;
     if (!allow_smem(score, tall ? done_tall : done_score, dev)) return PKV_ECUDA;
     if (units > 0x7fffffffll || (size_t)p.stride / 32 * 8 > kMaxDynamicSmem - sizeof(pkv::SelectSmem<512>))
         return PKV_EUNSUPPORTED;
     // three CTAs an SM, or as many as can have work
-    const long long tiles = units * ((p.stride + 7) / 8);
+    const long long tiles = units * ((p.stride + pkv::kScoreTile - 1) / pkv::kScoreTile);
     const long long ctas = std::max<long long>(
-        1, std::min<long long>(3ll * sm_count(dev), tiles / (pkv::kScoreMinTiles * pkv::kScoreWarps)));
+        1, std::min<long long>(3ll * sm_count(dev), tiles / pkv::kScoreWarps));
     OverlappedLaunch sc(ctas, pkv::kScoreThreads, pkv::ScoreSmem<D>::kAlloc, stream);
     if (cudaLaunchKernelEx(&sc.cfg, score, p) != cudaSuccess) return PKV_ECUDA;
     // scores in registers up to 8192 blocks; small CTAs where 1024 suffice
