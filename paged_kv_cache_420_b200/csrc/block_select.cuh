@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_blocks_kernel(const Se
                 if (k < len) issued = k + 1;
             }
         }
+        __syncthreads();  // the consumers are through
         // After a wait that gave up, what is in flight still has to land.
-        if (!ok && sub == 0)
+        if (*abort_flag && sub == 0)
             for (int k = max(0, issued - R); k < issued; ++k) mbar_wait_bounded(&full[j * R + k % R], (k / R) & 1, kWaitLimitNs);
-        grid_launch_dependents();
         return;
     }
     // -------------------------------------------------------- consumer --
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_blocks_kernel(const Se
                 make_float4(g0 ? sc[0] : -inf, g0 ? bound(sc[0]) : 0.f, g1 ? sc[1] : -inf, g1 ? bound(sc[1]) : 0.f);
         }
     }
-    grid_launch_dependents();
+    __syncthreads();
 }
 
 // ---------------------------------------------------------- selection ----

@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
                 ok = __all_sync(0xffffffffu, lane_ok);
             }
         }
+        named_barrier_sync(1, kDecodeThreads);  // the consumers are through
         // After a wait that gave up, what this lane has in flight still has to land.
-        if (!ok)
+        if (*abort_flag)
             for (int k = max(0, issued - kStreamGroup); k < issued; ++k)
                 if (k % kStreamGroup == sub) mbar_wait_bounded(&full[j * DEPTH + k % DEPTH], (k / DEPTH) & 1, kWaitLimitNs);
     } else {
@@ -757,7 +758,6 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
         named_barrier_sync(1, kDecodeThreads);  // every ring has run dry
         if (tail.unit >= 0) store_part(W + warp, ends + warp * (L::kPart / 4), L::kStride, tail);
     }
-    if (warp == W) named_barrier_sync(1, kDecodeThreads);
     __syncthreads();
     grid_launch_dependents();
 

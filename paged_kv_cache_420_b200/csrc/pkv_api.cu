@@ -271,7 +271,10 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
 
 constexpr int kStreamMaxCtas = 1184;  // 8 for each of 148 SMs
 constexpr int kStreamLong = 12;    // stages of a warp from which the line of selected blocks is cut anywhere
-constexpr int kStreamWhole = 16;   // stages of a unit up to which warps take whole units
+// Warps take whole units, so that nothing is merged, up to 4 stages a unit, and
+// up to 16 where every warp has one at least (10240 units of 1 to 8 stages: 54
+// us, 67 cut anywhere; a few units of 16 stages are faster cut).
+constexpr int kStreamWholeFew = 4, kStreamWhole = 16, kStreamWholeUnits = 2368;
 constexpr int kStreamRing = 48 << 10;      // bytes of a CTA's rings (e4m3: four CTAs an SM)
 constexpr int kStreamRingBf16 = 64 << 10;  // (bf16: three)
 
@@ -285,7 +288,7 @@ bool stream_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, long long stag
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || stages < 0) return false;
     const long long line = (long long)B * Hkv * (stages + pkv::kUnitCost);
     w->ctas = std::max<long long>(1, std::min<long long>(line / (pkv::kConsumerWarps * pkv::kMinCost), kStreamMaxCtas));
-    w->whole = stages <= kStreamWhole;
+    w->whole = stages <= kStreamWholeFew || (stages <= kStreamWhole && (long long)B * Hkv >= kStreamWholeUnits);
     const size_t heads = (size_t)w->ctas * 2 * (Hq / Hkv);
     w->off_ml = round256((size_t)w->ctas * sizeof(int2));
     w->off_acc = w->off_ml + round256(heads * sizeof(float2));
@@ -594,11 +597,15 @@ bool touch_grid(long long units, int W, unsigned *grid, unsigned *threads) {
 // Validates host pairs of a block copy: ids inside the pool, every destination
 // once and no pair's source.
 pkv_status check_pairs(const int32_t *src_dst_pairs, int32_t num_pairs, int32_t num_blocks) {
+    for (int i = 0; i < num_pairs; ++i) {
+        const int32_t s = src_dst_pairs[2 * i], d = src_dst_pairs[2 * i + 1];
+        if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) return PKV_ERANGE;
+    }
+    if (num_pairs > num_blocks) return PKV_EALIAS;  // some destination repeats
     std::vector<int32_t> src(num_pairs), dst(num_pairs);
     for (int i = 0; i < num_pairs; ++i) {
         src[i] = src_dst_pairs[2 * i];
         dst[i] = src_dst_pairs[2 * i + 1];
-        if (src[i] < 0 || src[i] >= num_blocks || dst[i] < 0 || dst[i] >= num_blocks) return PKV_ERANGE;
     }
     std::sort(src.begin(), src.end());
     std::sort(dst.begin(), dst.end());

@@ -1,5 +1,6 @@
 """Plain fp64 forms of the block-scaled cache and of block-sparse decode, and inputs for their tests (not
 collected as tests).  Loops over blocks and sequences, in numpy, from the definitions."""
+import functools
 import math
 
 import numpy as np
@@ -8,6 +9,16 @@ import torch
 import oracle
 
 E4M3_MAX = 448.0
+
+
+@functools.lru_cache(maxsize=None)
+def _table():
+    return oracle.e4m3_decode(np.arange(256, dtype=np.uint8))
+
+
+def decode(codes) -> np.ndarray:
+    """The values of e4m3 codes."""
+    return _table()[codes]
 
 
 def f64(t) -> np.ndarray:
@@ -42,7 +53,7 @@ def write(codes, scales, x, tables, ctx, start, bs):
                     was = scales[blk, h]
                     need = max(was, need)
                     if need > was:
-                        codes[blk, h] = oracle.e4m3_encode(oracle.e4m3_decode(codes[blk, h]) * (was / need))
+                        codes[blk, h] = oracle.e4m3_encode(decode(codes[blk, h]) * (was / need))
                 codes[blk, h, old:held] = oracle.e4m3_encode(rows / need)
                 scales[blk, h] = need
             j += 1
@@ -51,12 +62,12 @@ def write(codes, scales, x, tables, ctx, start, bs):
 
 def values(codes, scales):
     """The pool's values [NB, H, bs, D]."""
-    return oracle.e4m3_decode(codes) * np.asarray(scales, np.float64)[:, :, None, None]
+    return decode(codes) * np.asarray(scales, np.float64)[:, :, None, None]
 
 
 def same_codes(a, b):
     """Codes that stand for the same values (either NaN code is NaN, either zero is zero)."""
-    x, y = oracle.e4m3_decode(a), oracle.e4m3_decode(b)
+    x, y = decode(a), decode(b)
     return np.array_equal(x, y, equal_nan=True)
 
 
