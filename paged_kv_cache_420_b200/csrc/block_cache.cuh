@@ -89,7 +89,7 @@ struct WriteBlockParams {
     uint2 *v_cache;
     float *k_scales;  // [NB][H]
     float *v_scales;
-    long long units;  // B * J * H * 2
+    uint32_t units;   // B * J * H * 2
     int W;            // warps of a team
 };
 
@@ -147,13 +147,12 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
     __shared__ float s_amax[kTouchMaxWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wt = p.W > 1 ? warp : 0;  // warp of the team; several teams share a CTA only when W is 1
-    const long long u = p.W > 1 ? blockIdx.x : (long long)blockIdx.x * kTouchTeams + warp;
+    grid_dependency_wait();
+    const uint32_t u = p.W > 1 ? blockIdx.x : blockIdx.x * kTouchTeams + warp;
     if (u >= p.units) return;
     const int kv = (int)(u & 1);
-    long long r = u >> 1;
-    const int h = (int)(r % p.t.H);
-    r /= p.t.H;
-    const int i = (int)(r % p.t.J), s = (int)(r / p.t.J);
+    const uint32_t r = (u >> 1) / (uint32_t)p.t.H;
+    const int h = (int)((u >> 1) - r * p.t.H), s = (int)(r / (uint32_t)p.t.J), i = (int)(r - (uint32_t)s * p.t.J);
     TouchedBlock t;
     if (!touched_block(p.t, s, i, h == 0 && kv == 0 && wt == 0 && lane == 0, &t)) return;  // (the whole team)
     const size_t stride = (size_t)p.t.H * VPR;  // vectors between tokens
@@ -283,7 +282,7 @@ struct KeyBoundsParams {
     const void *k_cache;   // [NB][H][bs][D] bf16, or e4m3 codes
     const float *k_scales;  // [NB][H], e4m3 only
     uint4 *bounds;
-    long long units;  // B * J * H
+    uint32_t units;  // B * J * H
     int W;
 };
 
@@ -306,11 +305,11 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
     __shared__ uint4 s_lo[kTouchMaxWarps][VPR], s_hi[kTouchMaxWarps][VPR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wt = p.W > 1 ? warp : 0;
-    const long long u = p.W > 1 ? blockIdx.x : (long long)blockIdx.x * kTouchTeams + warp;
+    grid_dependency_wait();
+    const uint32_t u = p.W > 1 ? blockIdx.x : blockIdx.x * kTouchTeams + warp;
     if (u >= p.units) return;
-    const int h = (int)(u % p.t.H);
-    const long long r = u / p.t.H;
-    const int i = (int)(r % p.t.J), s = (int)(r / p.t.J);
+    const uint32_t r = u / (uint32_t)p.t.H;
+    const int h = (int)(u - r * p.t.H), s = (int)(r / (uint32_t)p.t.J), i = (int)(r - (uint32_t)s * p.t.J);
     TouchedBlock t;
     if (!touched_block(p.t, s, i, h == 0 && wt == 0 && lane == 0, &t)) return;  // (the whole team)
     const int sub = lane / VPR, c = lane % VPR;

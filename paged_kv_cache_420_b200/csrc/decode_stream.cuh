@@ -444,10 +444,10 @@ struct StreamSmem {
 };
 
 // CTAs of an SM that the registers must allow.
-constexpr int stream_min_ctas(int GPAD, bool KV8) { return GPAD > 8 ? 2 : KV8 ? 4 : 3; }
+constexpr int stream_min_ctas(int D, int GPAD, bool KV8) { return GPAD > 8 ? (D == 64 ? 3 : 2) : KV8 ? 4 : 3; }
 
 template <int D, int GPAD, int NS, bool KV8, bool SEL>
-__global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
+__global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(D, GPAD, KV8))
     stream_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                          const StreamParams p) {
     constexpr int W = kConsumerWarps;
@@ -877,27 +877,41 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(GPAD, KV8))
 }
 
 // --------------------------------------------------------------- reduce ----
-// CTA (c, head): where a unit ends in CTA c of the attention kernel and began in
-// an earlier one, that unit's records, that CTA's second one and the first ones
-// of the CTAs behind it, are merged by log-sum-exp.  Warp w takes records w, w +
-// 4, ...; lanes own D / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(kReduceWarps * 32) stream_reduce_kernel(const StreamParams p) {
+// Where a unit ends in CTA c of the attention kernel and began in an earlier
+// one, that unit's records, that CTA's second one and the first ones of the CTAs
+// behind it, are merged by log-sum-exp.  Block (i, head) looks at CTA i's note
+// or, BY_UNIT, for unit i's among the notes of `ctas` CTAs: few units leave many
+// records each, and take 16 warps to a row (one sequence of 131072 tokens, one
+// kv head, 512 records: 42 us in all with 4 warps, 29 with 16).  Warp w takes records w,
+// w + WARPS, ...; lanes own D / 32 elements.
+template <int D, int WARPS, bool BY_UNIT>
+__global__ void __launch_bounds__(WARPS * 32) stream_reduce_kernel(const StreamParams p, int ctas) {
     constexpr int EPL = D / 32;
-    __shared__ float s_o[kReduceWarps][D], s_l[kReduceWarps], s_m[kReduceWarps];
-    const int c = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ float s_o[WARPS][D], s_l[WARPS], s_m[WARPS];
+    __shared__ int s_c;
+    const int head = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int c = blockIdx.x;
+    if (tid == 0) s_c = -1;
     grid_dependency_wait();
+    if constexpr (BY_UNIT) {
+        __syncthreads();
+        for (int i = tid; i < ctas; i += WARPS * 32)
+            if (p.meta[i].x == (int)blockIdx.x) s_c = i;  // one at most
+        __syncthreads();
+        c = s_c;
+        if (c < 0) return;
+    }
     const int2 meta = p.meta[c];
     if (meta.x < 0) return;
     const int n = c - meta.y + 1;  // records
     auto record = [&](int i) { return ((size_t)(meta.y + i) * 2 + (i == 0)) * p.g + head; };
     float M = PKV_NEG_INF, acc[EPL], lsum = 0.f;
-    for (int i = warp + kReduceWarps * lane; i < n; i += kReduceWarps * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
+    for (int i = warp + WARPS * lane; i < n; i += WARPS * 32) M = fmaxf(M, p.rec_ml[record(i)].x);
     M = warp_max_f32(M);
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
 #pragma unroll 8
-    for (int i = warp; i < n; i += kReduceWarps) {
+    for (int i = warp; i < n; i += WARPS) {
         const size_t r = record(i);
         const float2 ml = p.rec_ml[r];
         const float f = ml.x == PKV_NEG_INF ? 0.f : ex2(ml.x - M);
@@ -919,9 +933,9 @@ __global__ void __launch_bounds__(kReduceWarps * 32) stream_reduce_kernel(const 
     if (tid < D) {
         float T = PKV_NEG_INF, Ls = 0.f, O = 0.f;
 #pragma unroll
-        for (int w = 0; w < kReduceWarps; ++w) T = fmaxf(T, s_m[w]);
+        for (int w = 0; w < WARPS; ++w) T = fmaxf(T, s_m[w]);
 #pragma unroll
-        for (int w = 0; w < kReduceWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const float f = s_m[w] == PKV_NEG_INF ? 0.f : ex2(s_m[w] - T);
             Ls = fmaf(s_l[w], f, Ls);
             O = fmaf(s_o[w][tid], f, O);

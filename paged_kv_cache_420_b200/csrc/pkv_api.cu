@@ -270,6 +270,7 @@ bool allow_smem(Kernel kernel, DeviceCache &done, int dev) {
 // ------------------------------------------------------- stream decode ----
 
 constexpr int kStreamMaxCtas = 1184;  // 8 for each of 148 SMs
+constexpr int kMergeByUnit = 64, kMergeWarps = 16;  // units up to which the merge goes by unit, with so many warps
 constexpr int kStreamLong = 12;    // stages of a warp from which the line of selected blocks is cut anywhere
 // Warps take whole units, so that nothing is merged, up to 4 stages a unit, and
 // up to 16 where every warp has one at least (10240 units of 1 to 8 stages: 54
@@ -341,9 +342,13 @@ pkv_status launch_stream(pkv::StreamParams prm, const StreamLayout &wl, void *wo
     OverlappedLaunch at(ctas, pkv::kDecodeThreads, L::kBytes, stream);
     if (cudaLaunchKernelEx(&at.cfg, kernel, mk, mv, prm) != cudaSuccess) return PKV_ECUDA;
     if (ctas > 1 && !prm.whole) {
-        OverlappedLaunch re(ctas, pkv::kReduceWarps * 32, 0, stream);
+        const long long units = (long long)prm.B * prm.Hkv;
+        const bool by_unit = units <= kMergeByUnit;
+        OverlappedLaunch re(by_unit ? units : ctas, (by_unit ? kMergeWarps : pkv::kReduceWarps) * 32, 0, stream);
         re.cfg.gridDim.y = (unsigned)prm.g;
-        if (cudaLaunchKernelEx(&re.cfg, pkv::stream_reduce_kernel<D>, prm) != cudaSuccess) return PKV_ECUDA;
+        const auto merge = by_unit ? pkv::stream_reduce_kernel<D, kMergeWarps, true>
+                                   : pkv::stream_reduce_kernel<D, pkv::kReduceWarps, false>;
+        if (cudaLaunchKernelEx(&re.cfg, merge, prm, ctas) != cudaSuccess) return PKV_ECUDA;
     }
     return launch_status();
 }
@@ -587,8 +592,8 @@ pkv_status touch_params(const pkv_pool &pool, const int32_t *block_tables, int32
 int touch_warps(const pkv_pool &pool) { return std::min(pool.block_size / pkv::kTouchRows, pkv::kTouchMaxWarps); }
 
 bool touch_grid(long long units, int W, unsigned *grid, unsigned *threads) {
+    if (units > 0x7fffffffll) return false;
     const long long ctas = W > 1 ? units : (units + pkv::kTouchTeams - 1) / pkv::kTouchTeams;
-    if (ctas > 0x7fffffffll) return false;
     *grid = (unsigned)ctas;
     *threads = 32u * (W > 1 ? W : pkv::kTouchTeams);
     return true;
@@ -937,19 +942,16 @@ pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *bloc
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     p.W = touch_warps(pool);
-    p.units = (long long)num_seqs * p.t.J * p.t.H * 2;
+    const long long units = (long long)num_seqs * p.t.J * p.t.H * 2;
     unsigned grid, threads;
-    if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!touch_grid(units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
+    p.units = (uint32_t)units;
     // the rows of a short append (a decode step) fit one pass: fewer registers
-    const int rows = p.t.max_new;
-    if (pool.head_dim == 128) {
-        if (rows <= 2) pkv::write_fp8_block_kernel<128, 1><<<grid, threads, 0, st>>>(p);
-        else pkv::write_fp8_block_kernel<128, 8><<<grid, threads, 0, st>>>(p);
-    } else {
-        if (rows <= 4) pkv::write_fp8_block_kernel<64, 1><<<grid, threads, 0, st>>>(p);
-        else pkv::write_fp8_block_kernel<64, 4><<<grid, threads, 0, st>>>(p);
-    }
+    const bool one = p.t.max_new <= (pool.head_dim == 128 ? 2 : 4);
+    const auto kernel = pool.head_dim == 128 ? (one ? pkv::write_fp8_block_kernel<128, 1> : pkv::write_fp8_block_kernel<128, 8>)
+                                             : (one ? pkv::write_fp8_block_kernel<64, 1> : pkv::write_fp8_block_kernel<64, 4>);
+    OverlappedLaunch la(grid, threads, 0, (cudaStream_t)stream);
+    if (cudaLaunchKernelEx(&la.cfg, kernel, p) != cudaSuccess) return PKV_ECUDA;
     return launch_status();
 }
 
@@ -1006,17 +1008,14 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
     p.k_scales = k_scales;
     p.bounds = static_cast<uint4 *>(bounds);
     p.W = touch_warps(pool);
-    p.units = (long long)num_seqs * p.t.J * p.t.H;
+    const long long units = (long long)num_seqs * p.t.J * p.t.H;
     unsigned grid, threads;
-    if (!touch_grid(p.units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (pool.head_dim == 128) {
-        if (kv8) pkv::key_bounds_kernel<128, true><<<grid, threads, 0, st>>>(p);
-        else pkv::key_bounds_kernel<128, false><<<grid, threads, 0, st>>>(p);
-    } else {
-        if (kv8) pkv::key_bounds_kernel<64, true><<<grid, threads, 0, st>>>(p);
-        else pkv::key_bounds_kernel<64, false><<<grid, threads, 0, st>>>(p);
-    }
+    if (!touch_grid(units, p.W, &grid, &threads)) return PKV_EUNSUPPORTED;
+    p.units = (uint32_t)units;
+    const auto kernel = pool.head_dim == 128 ? (kv8 ? pkv::key_bounds_kernel<128, true> : pkv::key_bounds_kernel<128, false>)
+                                             : (kv8 ? pkv::key_bounds_kernel<64, true> : pkv::key_bounds_kernel<64, false>);
+    OverlappedLaunch la(grid, threads, 0, (cudaStream_t)stream);
+    if (cudaLaunchKernelEx(&la.cfg, kernel, p) != cudaSuccess) return PKV_ECUDA;
     return launch_status();
 }
 
