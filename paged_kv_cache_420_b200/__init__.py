@@ -8,6 +8,7 @@ if libpkv.so is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -444,16 +445,29 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 _current_device = torch._C._cuda_getDevice
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+_WRITE_TYPES = (_BF16, _BF16, _I32, _I32, _I32, _F32, _F32, _U8, _U8)
+_DECODE_TYPES = (_BF16, _BF16, _U8, _U8, _F32, _F32, _I32, _I32)
+_BOUNDS_TYPES = (_I32, _I32, _I32, _BF16, _BF16)
+_BOUNDS_TYPES_FP8 = (_I32, _I32, _I32, _BF16, _U8, _F32)
+_SELECT_TYPES = (_BF16, _BF16, _I32, _I32, _I32)
+_SPARSE_TYPES = (_BF16, _BF16, _I32, _I32, _I32, _BF16, _BF16)
+_SPARSE_TYPES_FP8 = (_BF16, _BF16, _I32, _I32, _I32, _U8, _U8, _F32, _F32)
 
 
-def _tensors(*specs) -> int:
-    """Checks (tensor, name, dtype) triples, all contiguous and on one GPU, whose index it returns."""
-    index = specs[0][0].get_device()
-    for t, name, dtype in specs:
+def _tensors(names: str, dtypes, *tensors) -> int:
+    """Checks tensors against their types, all contiguous and on one GPU, whose index it returns."""
+    index = tensors[0].get_device()
+    for t, dtype in zip(tensors, dtypes):
         if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index or index < 0:
-            _need(t, name, dtype)
-            raise ValueError(f"{name}: all tensors must be on one device")
+            for t, name, dtype in zip(tensors, names.split(), dtypes):
+                _need(t, name, dtype)
+            raise ValueError(f"all tensors must be on one device: {names}")
     return index
+
+
+@functools.lru_cache(maxsize=64)
+def _pool_of(num_blocks, num_kv_heads, block_size, head_dim, kv_dtype):
+    return _Pool(num_blocks, num_kv_heads, block_size, head_dim, kv_dtype)
 
 
 def _launch(what: str, index: int, stream, f, *args) -> None:
@@ -510,10 +524,8 @@ def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Te
     """Appends and quantises: rows query_start[s] .. query_start[s+1] - 1 of k and v become the last positions of
     sequence s (context_lens counts them), as e4m3 codes with a power-of-two scale for each (block, kv head).  A
     block that already holds rows keeps its scale or grows it, and then its other codes are rounded anew."""
-    index = _tensors((k, "k", _BF16), (v, "v", _BF16), (block_tables, "block_tables", _I32),
-                     (context_lens, "context_lens", _I32), (query_start, "query_start", _I32),
-                     (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32), (k_cache, "k_cache", _U8),
-                     (v_cache, "v_cache", _U8))
+    index = _tensors("k v block_tables context_lens query_start k_scales v_scales k_cache v_cache", _WRITE_TYPES, k, v,
+                     block_tables, context_lens, query_start, k_scales, v_scales, k_cache, v_cache)
     B = _need_append(block_tables, context_lens, query_start)
     shape = nb, h, bs, d = _cache_sizes(k_cache)
     T = k.shape[0]
@@ -524,7 +536,7 @@ def pkv_write_fp8_block(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Te
     _launch("pkv_write_fp8_block", index, stream, load_library().pkv_write_fp8_block, k.data_ptr(), v.data_ptr(),
             block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), B, T,
             int(max_new_tokens), k_scales.data_ptr(), v_scales.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            _Pool(nb, h, bs, d, KV_E4M3))
+            _pool_of(nb, h, bs, d, KV_E4M3))
 
 
 def _scale_rows(k_scales, v_scales):
@@ -535,7 +547,7 @@ def _scale_rows(k_scales, v_scales):
 
 def pkv_copy_scales(src_dst_pairs, k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
     """Copies row src -> dst of both scale arrays for every (src, dst) host pair: pkv_copy_blocks' companion."""
-    index = _tensors((k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32))
+    index = _tensors("k_scales v_scales", (_F32, _F32), k_scales, v_scales)
     nb, h = _scale_rows(k_scales, v_scales)
     pairs = np.ascontiguousarray(np.asarray(src_dst_pairs, dtype=np.int32).reshape(-1, 2))
     _launch("pkv_copy_scales", index, stream, load_library().pkv_copy_scales, pairs.ctypes.data_as(ctypes.c_void_p),
@@ -546,8 +558,8 @@ def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: 
                     stream=None) -> None:
     """Copies row src -> dst of both scale arrays for the first num_pairs[0] rows of the device pair list: the
     companion of copy_blocks_dev."""
-    index = _tensors((cow_pairs, "cow_pairs", _I32), (num_pairs, "num_pairs", _I32), (k_scales, "k_scales", _F32),
-                     (v_scales, "v_scales", _F32))
+    index = _tensors("cow_pairs num_pairs k_scales v_scales", (_I32, _I32, _F32, _F32), cow_pairs, num_pairs, k_scales,
+                     v_scales)
     nb, h = _scale_rows(k_scales, v_scales)
     if cow_pairs.dim() != 2 or cow_pairs.shape[1] != 2 or num_pairs.numel() < 1:
         raise ValueError("cow_pairs must be [max_pairs, 2], num_pairs [1]")
@@ -555,6 +567,7 @@ def copy_scales_dev(cow_pairs: torch.Tensor, num_pairs: torch.Tensor, k_scales: 
             num_pairs.data_ptr(), cow_pairs.shape[0], k_scales.data_ptr(), v_scales.data_ptr(), nb, h)
 
 
+@functools.lru_cache(maxsize=256)
 def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                      max_context_len: int) -> int:
     n = load_library().pkv_decode_fp8_block_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -582,9 +595,8 @@ def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 scale: float, num_kv_heads: int, out: torch.Tensor, max_context_len: int,
                                 workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_attn_decode over an FP8 (e4m3) pool with a K and a V scale for each (block, kv head)."""
-    index = _tensors((q, "q", _BF16), (out, "out", _BF16), (k_cache, "k_cache", _U8), (v_cache, "v_cache", _U8),
-                     (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32), (block_tables, "block_tables", _I32),
-                     (context_lens, "context_lens", _I32))
+    index = _tensors("q out k_cache v_cache k_scales v_scales block_tables context_lens", _DECODE_TYPES, q, out,
+                     k_cache, v_cache, k_scales, v_scales, block_tables, context_lens)
     (B, Hq, D), (nb, h, bs, d) = _need_decode(q, out, k_cache, v_cache, block_tables, context_lens, num_kv_heads)
     if k_scales.shape != (nb, h) or v_scales.shape != (nb, h):
         raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
@@ -594,7 +606,7 @@ def paged_attn_decode_fp8_block(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     _launch("paged_attn_decode_fp8_block", index, stream, load_library().paged_attn_decode_fp8_block, q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
             block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), h, out.data_ptr(),
-            _Pool(nb, h, bs, d, KV_E4M3), max_context_len, ws, ws_bytes)
+            _pool_of(nb, h, bs, d, KV_E4M3), max_context_len, ws, ws_bytes)
 
 
 def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -606,9 +618,12 @@ def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_le
     fp8 = k_cache.dtype is _U8
     if (k_scales is not None) != fp8:
         raise ValueError("k_scales belong to an e4m3 pool, and only there")
-    specs = ((k_cache, "k_cache", _U8 if fp8 else _BF16), (block_tables, "block_tables", _I32),
-             (context_lens, "context_lens", _I32), (query_start, "query_start", _I32), (bounds, "bounds", _BF16))
-    index = _tensors(*specs, (k_scales, "k_scales", _F32)) if fp8 else _tensors(*specs)
+    names, tensors = "block_tables context_lens query_start bounds k_cache", (block_tables, context_lens, query_start,
+                                                                                 bounds, k_cache)
+    if fp8:
+        index = _tensors(names + " k_scales", _BOUNDS_TYPES_FP8, *tensors, k_scales)
+    else:
+        index = _tensors(names, _BOUNDS_TYPES, *tensors)
     B = _need_append(block_tables, context_lens, query_start)
     nb, h, bs, d = _cache_sizes(k_cache)
     if bounds.shape != (nb, h, 2, d):
@@ -618,9 +633,10 @@ def pkv_key_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_le
     _launch("pkv_key_bounds", index, stream, load_library().pkv_key_bounds, k_cache.data_ptr(),
             k_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
             context_lens.data_ptr(), query_start.data_ptr(), B, int(max_new_tokens), bounds.data_ptr(),
-            _Pool(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16))
+            _pool_of(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16))
 
 
+@functools.lru_cache(maxsize=256)
 def select_workspace_bytes(num_seqs: int, num_kv_heads: int, block_size: int, max_context_len: int) -> int:
     n = load_library().pkv_select_workspace_bytes(num_seqs, num_kv_heads, block_size, max_context_len)
     if n == 0:
@@ -634,8 +650,8 @@ def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch
     """selected[s][h] (int32 [B, num_kv_heads, K], K >= 2) := the logical blocks that decode attention of sequence s
     and kv head h keeps: the first, the last, and the best others by the upper bound of q.k that bounds
     (pkv_key_bounds) give, ascending; a context of at most K blocks keeps all, and -1 fills the row."""
-    index = _tensors((q, "q", _BF16), (bounds, "bounds", _BF16), (block_tables, "block_tables", _I32),
-                     (context_lens, "context_lens", _I32), (selected, "selected", _I32))
+    index = _tensors("q bounds block_tables context_lens selected", _SELECT_TYPES, q, bounds, block_tables,
+                     context_lens, selected)
     if q.dim() != 3 or bounds.dim() != 4 or selected.dim() != 3:
         raise ValueError("q must be [B, num_q_heads, head_dim], bounds [num_blocks, num_kv_heads, 2, head_dim] and "
                          "selected [B, num_kv_heads, num_selected]")
@@ -651,9 +667,10 @@ def pkv_select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_tables: torch
     ws, ws_bytes, keep = _scratch(workspace, need, index, stream)
     _launch("pkv_select_blocks", index, stream, load_library().pkv_select_blocks, q.data_ptr(), bounds.data_ptr(),
             block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, h,
-            _Pool(nb, h, bs, d, KV_BF16), selected.data_ptr(), K, max_context_len, ws, ws_bytes)
+            _pool_of(nb, h, bs, d, KV_BF16), selected.data_ptr(), K, max_context_len, ws, ws_bytes)
 
 
+@functools.lru_cache(maxsize=256)
 def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
                                   num_selected: int) -> int:
     n = load_library().pkv_decode_sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -673,10 +690,12 @@ def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
     fp8 = k_cache.dtype is _U8
     if (k_scales is not None) != fp8 or (v_scales is not None) != fp8:
         raise ValueError("k_scales and v_scales belong to an e4m3 pool, and only there")
-    cache = _U8 if fp8 else _BF16
-    specs = ((q, "q", _BF16), (out, "out", _BF16), (k_cache, "k_cache", cache), (v_cache, "v_cache", cache),
-             (block_tables, "block_tables", _I32), (context_lens, "context_lens", _I32), (selected, "selected", _I32))
-    index = _tensors(*specs, (k_scales, "k_scales", _F32), (v_scales, "v_scales", _F32)) if fp8 else _tensors(*specs)
+    names, tensors = "q out block_tables context_lens selected k_cache v_cache", (q, out, block_tables, context_lens,
+                                                                                     selected, k_cache, v_cache)
+    if fp8:
+        index = _tensors(names + " k_scales v_scales", _SPARSE_TYPES_FP8, *tensors, k_scales, v_scales)
+    else:
+        index = _tensors(names, _SPARSE_TYPES, *tensors)
     (B, Hq, D), (nb, h, bs, d) = _need_decode(q, out, k_cache, v_cache, block_tables, context_lens, num_kv_heads)
     if selected.dim() != 3 or selected.shape[0] != B or selected.shape[1] != h:
         raise ValueError("selected must be [B, num_kv_heads, num_selected]")
@@ -689,7 +708,7 @@ def paged_attn_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
             k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
             v_scales.data_ptr() if fp8 else None, block_tables.data_ptr(), block_tables.shape[1],
             context_lens.data_ptr(), selected.data_ptr(), K, B, Hq, float(scale), h, out.data_ptr(),
-            _Pool(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16), ws, ws_bytes)
+            _pool_of(nb, h, bs, d, KV_E4M3 if fp8 else KV_BF16), ws, ws_bytes)
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
