@@ -6,14 +6,22 @@
 // stretch of it, all of the same cost (a stage counts 1, a unit kUnitCost more
 // for its q, its first maxima and its output): no plan kernel, no work counter
 // and no partition size, however the lengths are spread, from one long
-// sequence to thousands of short ones.  A warp runs through the units of its stretch with one softmax state.  A unit
-// that lies within a stretch is written out by its warp; the parts of a unit
-// that stretches cut are merged in two steps, within the CTA (whose four
-// stretches are neighbours), then, where a unit goes on over CTAs, through at
-// most two records of each CTA that a second kernel merges.  Where all units
-// are short, the stretches end between units, and there is nothing to merge;
-// where units of equal length (selected blocks) are few, a cluster of CTAs takes
-// each and merges its parts through distributed shared memory.
+// sequence to thousands of short ones.  A warp runs through the units of its
+// stretch with one softmax state.  A unit that lies within a stretch is written
+// out by its warp; the parts of a unit that stretches cut are merged in two
+// steps, within the CTA (whose four stretches are neighbours), then, where a
+// unit goes on over CTAs, through at most two records of each CTA that a second
+// kernel merges.  Where all units are short, the stretches end between units,
+// and there is nothing to merge; where units of equal length (selected blocks)
+// are few, a cluster of CTAs takes each and merges its parts through
+// distributed shared memory.
+//
+// Bound by HBM on long lines: 8 sequences of 32768 to 131072 tokens, 64 query
+// heads on 8 (1.23 GB of codes), 199 to 205 us, 0.91 to 0.94 of the measured
+// copy rate; the warps of a fast CTA end 25% before those of the slowest, since
+// the stretches are fixed.  128 MHA sequences of 16 to 2048 tokens (0.53 GB) 101
+// us, 0.80.  Short lines are bound by the chain of loads before the first stage
+// (context, table, tiles: 4 us) and the merge.
 //
 //   dense:    unit (s, h) has ceil(context / 16) stages; each CTA adds up the
 //             contexts itself (they are few, and in L2)
@@ -409,8 +417,11 @@ struct StreamBound {
 struct __align__(16) StreamStage {
     int unit;
     int valid;  // tokens; 0: none (nothing was loaded)
-    int first;  // the first of its unit in this stretch: fresh state, q in the slot
-    int last;   // the last: 0 no, 1 the unit is complete, 2 its beginning was cut off, 4 its end is cut off, 8 + c: it began in CTA c and ends here
+    int first;  // the first of its unit in this stretch: fresh state and q
+    // The last of its unit in this stretch: 0 no, 1 the unit is complete, 2 its
+    // beginning was cut off, 4 its end is cut off, 8 + c: it began in CTA c and
+    // ends here.
+    int last;
 };
 
 template <int D, int GP, int NS, bool KV8>
@@ -436,11 +447,11 @@ struct StreamSmem {
     static constexpr int oScan = oInfo + NS * 16;                       // long long [threads][2]: stages, cost
     static constexpr int oWarpSum = oScan + kDecodeThreads * 16;
     static constexpr int oBounds = oWarpSum + (kW + 1) * 16;            // StreamBound [W + 1]
-    static constexpr int oOwn = kW * kPart;  // split: the CTA's partial, behind the parts in the rings
-    static_assert(oOwn % 16 == 0 && oOwn + GP * (D + 2) * 4 <= NS * kStage, "and the CTA's partial");
     static constexpr int oAbort = oBounds + (kW + 1) * (int)sizeof(StreamBound);
     static constexpr int kBytes = oAbort + 16;
-    static_assert(kW * kPart <= NS * kStage, "the parts at the stretches' ends fit into the rings");
+    static constexpr int oOwn = kW * kPart;  // split: the CTA's partial, behind the parts in the rings
+    static_assert(oOwn % 16 == 0 && oOwn + GP * (D + 2) * 4 <= NS * kStage,
+                  "the parts at the stretches' ends and the CTA's partial fit into the rings");
 };
 
 // CTAs of an SM that the registers must allow.
@@ -503,7 +514,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(D, GPAD, KV8))
     };
     const int spe = p.bs / kStageTok;  // stages of a block
     const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;  // sequences whose stages a thread adds up
-    auto stages_of = [&](int n) { return (n + kStageTok - 1) / kStageTok; };
+    auto stages_of = [&](int n) { return n / kStageTok + (n % kStageTok != 0); };
     longlong2 total;  // stages, cost
     if constexpr (SEL) {
         total.x = total.y = (long long)p.B * p.Hkv * p.K * spe;
@@ -647,7 +658,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(D, GPAD, KV8))
                 const int e = blk;
                 blk = __ldg(p.selected + (size_t)r.st.unit * p.K + e);
                 if (blk < 0) return r;
-                if (blk >= (n + p.bs - 1) / p.bs) {  // behind the context
+                if (blk >= n / p.bs + (n % p.bs != 0)) {  // behind the context
                     raise_error(PKV_DEVERR_BLOCK);
                     return r;
                 }
