@@ -410,7 +410,8 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *   lower index), num_selected in all, or every block of a shorter context.
  *   The ranking is that of scores in fp64; a NaN score counts as +infinity.
  *     q         bf16 [num_seqs][num_q_heads][head_dim], 16-B aligned
- *     bounds    as pkv_key_bounds leaves it (pool gives its sizes; either kv_dtype)
+ *     bounds    as pkv_key_bounds leaves it, lo <= hi (pool gives its sizes;
+ *               either kv_dtype)
  *     selected  int32 [num_seqs][num_kv_heads][num_selected], num_selected >= 2:
  *               ascending logical blocks, then -1
  *     max_context_len  host upper bound of context_lens (sizes the workspace;

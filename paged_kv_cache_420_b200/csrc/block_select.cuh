@@ -462,12 +462,15 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams &p, const __nv_
         const int j = j0 + (lane >> 3);
         double sum[2] = {0.0, 0.0};
         if (j < p.g) {
+            // the larger product is hi's where q is positive; both of them have
+            // to be numbers (an fp32 product is NaN where the exact one is)
             float x[E];
             load(q + (size_t)j * D, x);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const double y = (double)x[i] * (double)lo[i], z = (double)x[i] * (double)hi[i];
-                sum[i & 1] += (y != y || z != z) ? y + z : (y > z ? y : z);
+                const float y = x[i] * lo[i], z = x[i] * hi[i];
+                nan |= y != y || z != z;
+                sum[i & 1] = fma((double)x[i], (double)(x[i] > 0.f ? hi[i] : lo[i]), sum[i & 1]);
             }
         }
         double t = sum[0] + sum[1];
@@ -661,15 +664,20 @@ __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) 
         }
         __syncthreads();
     }
-    // the list, in ascending order
+    // the list, in ascending order: where each word's blocks begin, then a warp a
+    // word
     uint32_t at = 0;
     for (int base = 0; base < words; base += T) {
         const int w = base + tid;
-        uint32_t m = w < words ? kept[w] : 0, total;
-        uint32_t pos = at + block_scan<T>(sm, __popc(m), total);
+        uint32_t total;
+        const uint32_t pos = at + block_scan<T>(sm, w < words ? __popc(kept[w]) : 0, total);
         at += total;
-        for (; m != 0; m &= m - 1, ++pos)
-            if (pos < (uint32_t)p.K) out[pos] = w * 32 + __ffs(m) - 1;
+        if (w < words) open[w] = pos;
+    }
+    __syncthreads();
+    for (int w = warp; w < words; w += WARPS) {
+        const uint32_t m = kept[w], pos = open[w] + __popc(m & ((1u << lane) - 1));
+        if (((m >> lane) & 1u) && pos < (uint32_t)p.K) out[pos] = w * 32 + lane;
     }
 }
 
