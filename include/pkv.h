@@ -335,7 +335,9 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  *     new rows:   code = e4m3_rne_satfinite(x / s')
  *     the block's other rows, if it holds an older one and s' > scale:
  *                 code = e4m3_rne(e4m3(code) * scale / s')
- *   and s' becomes the block's scale.  (A grown scale takes the rows past the
+ *   and s' becomes the block's scale.  Both quotients are exact over scales that
+ *   are powers of two, as this call leaves them; over an older row's other
+ *   scales they are rounded to fp32 first.  (A grown scale takes the rows past the
  *   context along, so every code of the block keeps its value as nearly as it
  *   can.)  Infinities saturate, NaN stays NaN.  Rows past
  *   query_start[num_seqs] are not read; codes and scales of other blocks, and
@@ -429,7 +431,8 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *               logical blocks in any order; a negative entry is none, an entry
  *               behind the context's last block sets PKV_DEVERR_BLOCK and is
  *               none, and a block listed twice counts twice.  No valid entry
- *               (or an empty context) gives a zero output row.
+ *               (or an empty context) gives a zero output row, and so do keys
+ *               whose scores are all -infinity.
  *     k_scales, v_scales  NULL for a bf16 pool; the block scales of an e4m3 pool
  *   Both pools at head dimensions 64 and 128 and every GQA group <= 16, with
  *   fp32 sums; the weights enter the weighted sum rounded to 17 bits over a

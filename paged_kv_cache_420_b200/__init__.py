@@ -490,16 +490,19 @@ def _launch(what: str, index: int, stream, f, *args) -> None:
 
 
 def _scratch(workspace: Optional[torch.Tensor], nbytes: int, index: int, stream):
-    """(address, bytes, keeper) of a call's workspace: the caller's, or a new one for `stream` (None: the current
-    one).  The keeper has to live until the call is enqueued."""
+    """(address, bytes, keeper) of a call's workspace: the caller's, or a new one.  The keeper has to live until the
+    call is enqueued."""
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != index:
             raise ValueError("workspace must be contiguous and on the other tensors' device")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    ws = torch.empty(nbytes, dtype=_U8, device=index)
-    if stream is not None:  # the allocator may hand the memory on once `stream` is through, not before
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index))
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=_U8, device=index)
+    else:  # `stream`'s memory: what the current stream has let go of may still be in use there
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=_U8, device=index)
     return ws.data_ptr(), nbytes, ws
 
 

@@ -41,6 +41,10 @@ namespace pkv {
 
 // ------------------------------------------------------------- arithmetic ----
 
+// Where the references begin: the least finite number, so that a score of
+// -infinity weighs 0 from the first stage on (-infinity would leave NaN there).
+constexpr float kNoScore = -3.402823466e38f;
+
 // The power of two that brings a largest magnitude into [1, 2) (1/2 .. 4 at
 // the ends of the range): q is converted to f16 with it, so its elements keep
 // 11 bits down to 2^-14 of the head's largest whatever their size.  The
@@ -105,7 +109,7 @@ struct TileState {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) { m[nt][c] = PKV_NEG_INF; m2[nt][c] = PKV_NEG_INF; l[nt][c] = 0.f; }
+            for (int c = 0; c < 2; ++c) { m[nt][c] = kNoScore; m2[nt][c] = kNoScore; l[nt][c] = 0.f; }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -323,7 +327,7 @@ struct TileState {
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-        f = !KV8 ? 1.f : m2[nt][c] == PKV_NEG_INF ? 0.f : ex2(m2[nt][c] - m[nt][c]);
+        f = KV8 ? ex2(m2[nt][c] - m[nt][c]) : 1.f;
     }
 
     // This warp's part (m, l, O) of a unit: rows of `stride` floats.
@@ -792,8 +796,7 @@ __global__ void __launch_bounds__(kDecodeThreads, stream_min_ctas(D, GPAD, KV8))
 #pragma unroll
         for (int y = 0; y < 2 * W; ++y)
             if (part_info[y].unit == unit) M = fmaxf(M, mM[y * GP + hd]);
-        const float mu = mM[part_at(x) * GP + hd];
-        factor[x * GP + hd] = mu == PKV_NEG_INF ? 0.f : ex2(mu - M);
+        factor[x * GP + hd] = ex2(mM[part_at(x) * GP + hd] - M);
     }
     if (tid == 0 && !(SEL && p.split)) p.meta[blockIdx.x] = make_int2(-1, 0);
     __syncthreads();

@@ -373,7 +373,7 @@ bool select_layout(int32_t B, int32_t H, int32_t bs, int32_t max_ctx, SelectLayo
     w->stride = std::max<long long>(32, (((long long)max_ctx + bs - 1) / bs + 31) / 32 * 32);
     const size_t units = (size_t)B * H;
     w->off_keys = round256(units * w->stride * sizeof(float2));
-    w->total = w->off_keys + round256(units * w->stride * sizeof(uint64_t));
+    w->total = std::max<size_t>(256, w->off_keys + round256(units * w->stride * sizeof(uint64_t)));
     return true;
 }
 

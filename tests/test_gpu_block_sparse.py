@@ -217,6 +217,32 @@ def test_sparse_reads_only_what_is_selected(fp8, g):
     no_device_error()
 
 
+@pytest.mark.parametrize("g,K", [(1, 40), (4, 40), (16, 40), (8, 2)])
+def test_sparse_scores_of_minus_infinity(g, K):
+    """Keys that lead to scores of -infinity (or below fp32's range) weigh nothing, wherever they come in a warp's
+    stretch; a row of nothing else is zero."""
+    b = batch([16 * 50, 16 * 3 + 5], 2, g, 128, 16, seed=8)
+    b.q[..., 0] = b.q[..., 0].abs() + 0.5
+    sel = np.full((2, 2, K), -1, np.int32)
+    sel[0] = np.random.default_rng(8).permutation(50)[:K]
+    sel[1, :, 0] = 3
+    k, v = b.bf16_pool()
+    left = sel.copy()
+    low = [(0, j) for j in (sel[0, 0, 0], sel[0, 0, K // 2], sel[0, 0, K - 1])[:K // 2]] + [(1, 3)]
+    for i, (s, j) in enumerate(low):
+        k[b.tables[s, j], :, :, 0] = float("-inf")
+        if i == 1:  # finite keys, whose scores overflow
+            k[b.tables[s, j], :, :, 0] = torch.finfo(torch.bfloat16).min
+            b.q[s, :, 0] = 8.0
+        left[s][left[s] == j] = -1
+    out = torch.empty((2, 2 * g, 128), dtype=torch.bfloat16, device="cuda")
+    pkv.paged_attn_decode_sparse(cuda(b.q), cuda(k), cuda(v), cuda(b.tables), cuda(b.ctx), cuda(sel), b.scale, 2, out)
+    want = ref.attend(ref.f64(b.q), ref.f64(k), ref.f64(v), b.tables, b.ctx, b.scale, 16, left)
+    ref.assert_attention(out, want, 2.0 ** -16)
+    assert (out[1] == 0).all()
+    no_device_error()
+
+
 def test_sparse_reports_bad_entries():
     b = batch([100, 64], 1, 2, 64, 16, seed=4)
     sel = np.array([[[0, 6, 7, 2]], [[0, 4, 1, 2 ** 31 - 1]]], np.int32)  # 7 and 4 lie behind the contexts
@@ -243,6 +269,47 @@ def test_all_blocks_selected_is_dense_decode(g):
                       v_scales=b.vs)
     ref.assert_attention(dense, want, 2.0 ** -11)
     no_device_error()
+
+
+@pytest.mark.parametrize("scale", [-0.25, 0.0])
+def test_any_scale(scale):
+    b = batch([900, 31], 2, 4, 128, 16, seed=15)
+    b.scale = scale
+    for fp8 in (False, True):
+        check_sparse(b, random_selection(b, 30, 2), fp8)
+
+
+def test_empty_batch():
+    """No sequences: every call returns, with a workspace of its own making too."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ctx, tables, start = torch.zeros(0, **i32), torch.zeros((0, 4), **i32), torch.zeros(1, **i32)
+    q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((4, 2, 16, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((4, 2), device="cuda")
+    bounds = torch.zeros((4, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    sel, rows = torch.zeros((0, 2, 3), **i32), q[:, :2].contiguous()
+    pkv.pkv_write_fp8_block(rows, rows, tables, ctx, start, scales, scales, codes, codes, 1)
+    pkv.pkv_key_bounds(codes, tables, ctx, start, bounds, 1, scales)
+    pkv.pkv_select_blocks(q, bounds, tables, ctx, 2, 16, sel, 64)
+    pkv.paged_attn_decode_sparse(q, codes, codes, tables, ctx, sel, 1.0, 2, q, scales, scales)
+    pkv.paged_attn_decode_fp8_block(q, codes, codes, scales, scales, tables, ctx, 1.0, 2, q, 64)
+    torch.cuda.synchronize()
+    assert (codes == 0).all() and (bounds == 0).all()
+    no_device_error()
+
+
+def test_workspace_for_another_stream_is_that_streams_memory():
+    """What the current stream has let go of may still be in use there, so a call for another stream takes none of
+    it."""
+    torch.cuda.empty_cache()
+    stream, n = torch.cuda.Stream(), 24 << 20
+    device = torch.cuda.current_device()
+    for other in (stream, stream.cuda_stream):
+        held = torch.empty(n, dtype=torch.uint8, device="cuda")
+        at = held.data_ptr()
+        del held
+        assert pkv._scratch(None, n, device, None)[0] == at
+        assert pkv._scratch(None, n, device, other)[0] != at
 
 
 def test_two_calls_at_once_give_the_same_results():
