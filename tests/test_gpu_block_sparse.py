@@ -312,6 +312,42 @@ def test_workspace_for_another_stream_is_that_streams_memory():
         assert pkv._scratch(None, n, device, other)[0] != at
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+def test_blocks_past_4_gib_of_the_pool(fp8):
+    """The same step at the lowest and at the highest block ids of pools of more than 2^32 bytes: every result repeats
+    bit for bit."""
+    H, g, D, bs, n = 8, 2, 128, 16, 40
+    NB = (2 ** 32 // (H * bs * D)) // (1 if fp8 else 2) + 64
+    keys, vals = (torch.empty((NB, H, bs, D), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda") for _ in "kv")
+    ks, vs = (torch.ones((NB, H), device="cuda") if fp8 else None for _ in "kv")
+    bounds = torch.empty((NB, H, 2, D), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(21)
+    x = cuda(torch.randn((bs * n, H, D), generator=gen).to(torch.bfloat16))
+    q = cuda(torch.randn((1, H * g, D), generator=gen).to(torch.bfloat16))
+    ctx, start = cuda(np.array([bs * n], np.int32)), cuda(np.array([0, bs * n], np.int32))
+    got = []
+    for first in (0, NB - n):
+        tables = cuda(np.arange(first, first + n, dtype=np.int32)[None])
+        if fp8:
+            pkv.pkv_write_fp8_block(x, x, tables, ctx, start, ks, vs, keys, vals, bs * n)
+        else:
+            keys[first:first + n] = vals[first:first + n] = x.view(n, bs, H, D).transpose(1, 2)
+        pkv.pkv_key_bounds(keys, tables, ctx, start, bounds, bs * n, ks)
+        sel = torch.empty((1, H, 9), dtype=torch.int32, device="cuda")
+        pkv.pkv_select_blocks(q, bounds, tables, ctx, H, bs, sel, bs * n)
+        out = [torch.zeros_like(q), torch.zeros_like(q)]
+        pkv.paged_attn_decode_sparse(q, keys, vals, tables, ctx, sel, 0.1, H, out[0], ks, vs)
+        if fp8:
+            pkv.paged_attn_decode_fp8_block(q, keys, vals, ks, vs, tables, ctx, 0.1, H, out[1], bs * n)
+        # a code is half a step off at most: 2^-4 of its value, or 2^-10 of a scale that is 2^-6 at most here
+        top, most = bounds[first:first + n, :, 1].float(), x.view(n, bs, H, D).amax(1).float()
+        assert ((top - most).abs() <= (most.abs() / 16 + 2.0 ** -16 if fp8 else 0)).all()
+        got.append((keys[first:first + n].clone(), vals[first:first + n].clone(), bounds[first:first + n].clone(), sel, *out))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    no_device_error()
+
+
 def test_two_calls_at_once_give_the_same_results():
     """No state outside a call's arguments: calls that overlap on two streams repeat bit for bit what each gives
     alone."""
