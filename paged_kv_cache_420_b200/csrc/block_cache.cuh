@@ -274,9 +274,14 @@ __global__ void __launch_bounds__(256) copy_scales_dev_kernel(float *k_scales, f
 // lo[d] = min, hi[d] = max over the held rows of a (block, head), NaN if one
 // of them is NaN; [NB][H][2][D] bf16, lo first.  Every held row is read, not
 // only the new ones: a block that was copied or whose scale has grown needs no
-// other care.  Over an 8-bit pool the least and largest CODE are found (exact
-// as f16; the scale is positive, and rounding to bf16 keeps the order) and
-// scaled once.
+// other care.  Over an 8-bit pool the least and largest CODE are found and
+// scaled once (the scale is positive, and rounding to bf16 keeps the order).
+// Sign-magnitude numbers order alike whatever their fields, so a code is
+// compared as the upper byte of a bf16: what lies in the lower one decides
+// between equal codes only, and 0x7f and 0xff, the NaN codes, stay at an end or
+// become a bf16 NaN, whose upper byte is 0x7f.  8 prompts of 2048 to 8192
+// tokens, 8 heads: 9.1 us, 9.7 with codes converted to f16 first, 10.5 as integers
+// (which take a third extreme).
 struct KeyBoundsParams {
     TouchParams t;
     const void *k_cache;   // [NB][H][bs][D] bf16, or e4m3 codes
@@ -286,21 +291,22 @@ struct KeyBoundsParams {
     int W;
 };
 
-template <bool F16>
-__device__ __forceinline__ void min_max_x2(uint32_t &lo, uint32_t &hi, uint32_t l, uint32_t h) {
-    if constexpr (F16) {
-        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(l));
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(h));
-    } else {
-        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(l));
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(h));
-    }
+__device__ __forceinline__ void min_max_bf16x2(uint32_t &lo, uint32_t &hi, uint32_t l, uint32_t h) {
+    asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(l));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(h));
+}
+
+// The upper bytes of `even` and `odd`, codes of columns 0, 2 and 1, 3, as values.
+__device__ __forceinline__ void values_of_codes(uint32_t even, uint32_t odd, float (&x)[4]) {
+    const float2 a = f32x2_from_f16x2(f16x2_from_e4m3x2(__byte_perm(even, odd, 0x4451)));
+    const float2 b = f32x2_from_f16x2(f16x2_from_e4m3x2(__byte_perm(even, odd, 0x4473)));
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
 template <int D, bool KV8>
 __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const KeyBoundsParams p) {
     constexpr int VPR = D / 8, RPP = 32 / VPR, PASSES = kTouchRows / RPP;
-    constexpr uint32_t kPosInf = KV8 ? 0x7c007c00u : 0x7f807f80u, kNegInf = KV8 ? 0xfc00fc00u : 0xff80ff80u;
+    constexpr uint32_t kPosInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
     using Vec = typename std::conditional<KV8, uint2, uint4>::type;
     __shared__ uint4 s_lo[kTouchMaxWarps][VPR], s_hi[kTouchMaxWarps][VPR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -329,15 +335,12 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
         for (int q = 0; q < PASSES; ++q) {
             uint32_t w[4];
             if constexpr (KV8) {
-                w[0] = f16x2_from_e4m3x2(in[q].x & 0xffffu);
-                w[1] = f16x2_from_e4m3x2(in[q].x >> 16);
-                w[2] = f16x2_from_e4m3x2(in[q].y & 0xffffu);
-                w[3] = f16x2_from_e4m3x2(in[q].y >> 16);
+                w[0] = in[q].x << 8; w[1] = in[q].x; w[2] = in[q].y << 8; w[3] = in[q].y;
             } else {
                 w[0] = in[q].x; w[1] = in[q].y; w[2] = in[q].z; w[3] = in[q].w;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) min_max_x2<KV8>(lo[e], hi[e], w[e], w[e]);
+            for (int e = 0; e < 4; ++e) min_max_bf16x2(lo[e], hi[e], w[e], w[e]);
         }
     }
 #pragma unroll
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t l = __shfl_xor_sync(0xffffffffu, lo[e], o), g = __shfl_xor_sync(0xffffffffu, hi[e], o);
-            min_max_x2<KV8>(lo[e], hi[e], l, g);
+            min_max_bf16x2(lo[e], hi[e], l, g);
         }
     }
     if (p.W > 1) {
@@ -357,18 +360,28 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
         if (wt != 0) return;
         for (int w = 1; w < p.W; ++w) {
             const uint4 l = s_lo[w][c], g = s_hi[w][c];
-            min_max_x2<KV8>(lo[0], hi[0], l.x, g.x);
-            min_max_x2<KV8>(lo[1], hi[1], l.y, g.y);
-            min_max_x2<KV8>(lo[2], hi[2], l.z, g.z);
-            min_max_x2<KV8>(lo[3], hi[3], l.w, g.w);
+            min_max_bf16x2(lo[0], hi[0], l.x, g.x);
+            min_max_bf16x2(lo[1], hi[1], l.y, g.y);
+            min_max_bf16x2(lo[2], hi[2], l.z, g.z);
+            min_max_bf16x2(lo[3], hi[3], l.w, g.w);
         }
     }
     if constexpr (KV8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 l = f32x2_from_f16x2(lo[e]), g = f32x2_from_f16x2(hi[e]);
-            lo[e] = pack_bf16x2(l.x * ks, l.y * ks);
-            hi[e] = pack_bf16x2(g.x * ks, g.y * ks);
+        for (int v = 0; v < 4; v += 2) {  // word v / 2 of the row's codes
+            float l[4], g[4];
+            values_of_codes(lo[v], lo[v + 1], l);
+            values_of_codes(hi[v], hi[v + 1], g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool nan = l[e] != l[e] || g[e] != g[e];
+                l[e] = nan ? __int_as_float(0x7fffffff) : l[e] * ks;
+                g[e] = nan ? __int_as_float(0x7fffffff) : g[e] * ks;
+            }
+            lo[v] = pack_bf16x2(l[0], l[1]);
+            lo[v + 1] = pack_bf16x2(l[2], l[3]);
+            hi[v] = pack_bf16x2(g[0], g[1]);
+            hi[v + 1] = pack_bf16x2(g[2], g[3]);
         }
     }
     if (lane < VPR) {

@@ -177,6 +177,26 @@ def test_key_bounds_of_nan_and_infinite_keys():
     no_device_error()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [16, 48])
+def test_key_bounds_of_every_code(D, bs):
+    """Any code beside any other: columns of one sign, of zeros of both signs, of the largest codes, with a NaN of
+    either sign."""
+    r = np.random.default_rng(17)
+    b = ref.Batch([bs * 5 - 3, 2], [bs * 5 - 3, 2], 3, D, bs, seed=16)
+    kinds = [np.arange(256), np.arange(0x7F), 0x80 + np.arange(0x7F), [0, 0x80], [0x7C, 0x7D, 0x7E], [0xFC, 0xFD, 0xFE],
+             [0x7E, 0xFE, 0x7F], [0xFE, 0xFF], [0x01, 0x81, 0x00]]
+    for blk in range(b.NB):
+        for h in range(3):
+            for d in range(D):
+                b.kc[blk, h, :, d] = r.choice(np.asarray(kinds[r.integers(len(kinds))], np.uint8), bs)
+    got = torch.zeros((b.NB, 3, 2, D), dtype=torch.bfloat16, device="cuda")
+    pkv.pkv_key_bounds(cuda(b.kc), cuda(b.tables), cuda(b.ctx), cuda(b.start), got, bs * 5, k_scales=cuda(b.ks))
+    want = ref.key_bounds(np.zeros(got.shape), ref.values(b.kc, b.ks), b.tables, b.ctx, b.start, bs)
+    assert np.array_equal(ref.f64(got), want, equal_nan=True)
+    no_device_error()
+
+
 def run_decode(b, q=None, stream=None, workspace=None):
     out = torch.full((len(b.ctx), b.H * b.g, b.D), float("nan"), dtype=torch.bfloat16, device="cuda")
     pkv.paged_attn_decode_fp8_block(cuda(b.q if q is None else q), cuda(b.kc), cuda(b.vc), cuda(b.ks), cuda(b.vs),
