@@ -12,6 +12,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "block_cache.cuh"
@@ -607,7 +608,13 @@ pkv_status check_pairs(const int32_t *src_dst_pairs, int32_t num_pairs, int32_t 
         if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) return PKV_ERANGE;
     }
     if (num_pairs > num_blocks) return PKV_EALIAS;  // some destination repeats
-    std::vector<int32_t> src(num_pairs), dst(num_pairs);
+    std::vector<int32_t> src, dst;
+    try {
+        src.resize(num_pairs);
+        dst.resize(num_pairs);
+    } catch (const std::bad_alloc &) {  // no exception leaves a C entry
+        return PKV_EUNSUPPORTED;
+    }
     for (int i = 0; i < num_pairs; ++i) {
         src[i] = src_dst_pairs[2 * i];
         dst[i] = src_dst_pairs[2 * i + 1];
