@@ -492,7 +492,7 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams &p, const __nv_
 template <int D, int T, int PER>
 __global__ void __launch_bounds__(T) select_blocks_kernel(const SelectParams p) {
     constexpr int WARPS = T / 32;
-    constexpr int kBits = T == 512 ? 11 : 9;  // of 4 T bins
+    constexpr int kBits = T == 512 ? 11 : T == 256 ? 10 : T == 128 ? 9 : 8;  // of 4 T bins
     static_assert(4 * T == 1 << kBits, "bins");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     SelectSmem<T> *sm = reinterpret_cast<SelectSmem<T> *>(smem_raw);

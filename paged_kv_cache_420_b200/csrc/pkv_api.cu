@@ -407,10 +407,16 @@ pkv_status launch_select(const pkv::SelectParams &p, long long units, cudaStream
     OverlappedLaunch sc(ctas, pkv::kScoreThreads, pkv::ScoreSmem<D>::kAlloc, stream);
     if (cudaLaunchKernelEx(&sc.cfg, score, p) != cudaSuccess) return PKV_ECUDA;
     // Scores in registers up to 8192 blocks (8 sequences of up to 131072 tokens,
-    // 8 heads, scoring included: 42.8 us, 44.3 with scores read again); small
-    // CTAs where 1024 suffice (64 sequences of up to 8192: 22.5, 39.9 with 512
-    // threads each).
+    // 8 heads, scoring included: 42.8 us, 44.3 with scores read again), and CTAs
+    // as small as that allows, so that many share an SM (64 sequences of up to
+    // 8192 tokens: 22.5, 39.9 with 512 threads each; 128 of up to 20000: 62 and 95;
+    // 32 of up to 65536: 85 and 91), but where an SM has one anyway (4 of
+    // those: 21.5, 23.5 with 256 threads; of 128 blocks at most, 5120 heads: 52 with
+    // 64 threads, 60 with 128, but 64 heads: 11.8 and 11.0).
+    if (p.stride <= 128 && units > 8ll * sm_count(dev)) return launch_selection<D, 64, 2>(p, units, stream, dev);
     if (p.stride <= 1024) return launch_selection<D, 128, 8>(p, units, stream, dev);
+    if (p.stride <= 2048) return launch_selection<D, 256, 8>(p, units, stream, dev);
+    if (p.stride <= 4096 && units > sm_count(dev)) return launch_selection<D, 256, 16>(p, units, stream, dev);
     if (p.stride <= 8192) return launch_selection<D, 512, 16>(p, units, stream, dev);
     return launch_selection<D, 512, 0>(p, units, stream, dev);
 }

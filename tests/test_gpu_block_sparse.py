@@ -64,6 +64,18 @@ def test_select(ctx, H, g, D, bs, K):
     check_select(b, random_bounds(b, sum(ctx)), K)
 
 
+@pytest.mark.parametrize("ctx,H,K", [
+    ([16 * 2100 + 37 * i for i in range(5)], 32, 8),                # 160 heads of over 2048 blocks
+    ([40 + 13 * i % 1900 for i in range(155)], 8, 5),               # 1240 heads of up to 122 blocks
+])
+def test_select_of_many_heads(ctx, H, K):
+    """Where there are more heads than an SM takes at once, smaller CTAs select: the same blocks, ties included."""
+    b = batch(ctx, H, 1, 64, 16, seed=len(ctx))
+    bounds = random_bounds(b, H)
+    check_select(b, bounds, K)
+    check_select(b, bounds[:3][torch.arange(b.NB) % 3].contiguous(), K)
+
+
 @pytest.mark.parametrize("n,K", [(40, 9), (600, 100), (3000, 1500), (8500, 700)])
 def test_select_ties(n, K):
     """Equal scores go to the lower index: all bounds alike (more undecided blocks than are compared one by one),
