@@ -321,13 +321,15 @@ struct TileState {
         }
     }
 
-    // l summed over its lanes, and what brings a column of O^T to reference m.
+    // l summed over its lanes, and what brings a column of O^T to reference m:
+    // f twice, each half of the exponent, since m2 - m leaves fp32's range where
+    // V's scales lie at its ends (2^-126 is a block's of zeros).
     __device__ __forceinline__ void finish(int nt, int c, float &lsum, float &f) {
         lsum = l[nt][c];
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-        f = KV8 ? ex2(m2[nt][c] - m[nt][c]) : 1.f;
+        f = KV8 ? ex2(0.5f * (m2[nt][c] - m[nt][c])) : 1.f;
     }
 
     // This warp's part (m, l, O) of a unit: rows of `stride` floats.
@@ -344,8 +346,8 @@ struct TileState {
                 float *row = acc + head * stride + (lane >> 2);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    row[mt * 16] = o[nt][mt][c] * f;
-                    row[mt * 16 + 8] = o[nt][mt][c + 2] * f;
+                    row[mt * 16] = KV8 ? o[nt][mt][c] * f * f : o[nt][mt][c];
+                    row[mt * 16 + 8] = KV8 ? o[nt][mt][c + 2] * f * f : o[nt][mt][c + 2];
                 }
             }
     }
@@ -354,19 +356,20 @@ struct TileState {
     __device__ __forceinline__ void write_out(__nv_bfloat16 *out, int lane, int g) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float f[2];
+            float f[2], fl[2];  // O f fl is the row
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float lsum;
                 finish(nt, c, lsum, f[c]);
-                f[c] = lsum > 0.f || lsum != lsum ? __fdividef(f[c], lsum) : 0.f;
+                fl[c] = lsum > 0.f || lsum != lsum ? __fdividef(f[c], lsum) : 0.f;
             }
+            auto value = [&](float x, int c) { return KV8 ? x * f[c] * fl[c] : x * fl[c]; };
             const int head = nt * 8 + (lane >> 2);  // after the transpose
             uint32_t *row = reinterpret_cast<uint32_t *>(out + head * D + 2 * (lane & 3));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t x = movmatrix_trans(pack_bf16x2(o[nt][mt][0] * f[0], o[nt][mt][1] * f[1]));
-                const uint32_t y = movmatrix_trans(pack_bf16x2(o[nt][mt][2] * f[0], o[nt][mt][3] * f[1]));
+                const uint32_t x = movmatrix_trans(pack_bf16x2(value(o[nt][mt][0], 0), value(o[nt][mt][1], 1)));
+                const uint32_t y = movmatrix_trans(pack_bf16x2(value(o[nt][mt][2], 0), value(o[nt][mt][3], 1)));
                 if (head < g) {
                     row[mt * 8] = x;
                     row[mt * 8 + 4] = y;

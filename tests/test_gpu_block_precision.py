@@ -1,0 +1,77 @@
+"""The block-scaled cache and block-sparse decode at the ends of their types' ranges: small weights beside a large
+one, queries with one large element, the least V scales, infinite values, old scales that are no powers of two."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_cache_420_b200 as pkv
+from tests import _block_ref as ref
+from tests._gpu_util import no_device_error
+
+pytestmark = pytest.mark.gpu
+
+ONE = 0x38  # the e4m3 code of 1
+
+
+def cuda(x):
+    return (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).cuda()
+
+
+def one_warp(ctx, H, g, D, seed):
+    """Contexts of at most 64 tokens, which one warp takes alone; no key differs from another yet."""
+    b = ref.Batch(ctx, [1] * len(ctx), H, D, 16, seed=seed, g=g)
+    b.kc[:], b.ks[:] = 0, 1.0
+    return b
+
+
+def decode(b, sel=None):
+    out = torch.full((len(b.ctx), b.H * b.g, b.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    pool = [cuda(x) for x in (b.kc, b.vc, b.ks, b.vs)]
+    if sel is None:
+        pkv.paged_attn_decode_fp8_block(cuda(b.q), *pool, cuda(b.tables), cuda(b.ctx), b.scale, b.H, out, int(b.ctx.max()))
+    else:
+        pkv.paged_attn_decode_sparse(cuda(b.q), *pool[:2], cuda(b.tables), cuda(b.ctx), cuda(sel), b.scale, b.H, out,
+                                     k_scales=pool[2], v_scales=pool[3])
+    torch.cuda.synchronize()
+    return out
+
+
+def check(b, what, out_step=2.0 ** -8):
+    """Dense, and with every block selected.  |got - out| within `_block_ref.assert_attention`'s roundings, but an f16
+    product is at most 2^15 where the reference of its column is 1 * 2^7, so its spacing of 2^-24 below 2^-14 is 2^-31
+    of the largest product, and half of that is what a product is off by at most; and bf16's own spacing below its
+    normal range, 2^-133, in place of an absolute term."""
+    n = b.tables.shape[1]
+    every = np.where(np.arange(n) * b.bs < b.ctx[:, None], np.arange(n), -1)
+    sel = np.ascontiguousarray(np.broadcast_to(every[:, None], (len(b.ctx), b.H, n)).astype(np.int32))
+    out, weight, zmag, unit = ref.attend(ref.f64(b.q), ref.values(b.kc, b.ks), ref.values(b.vc, b.vs), b.tables, b.ctx,
+                                         b.scale, b.bs, v_scales=b.vs)
+    dz = 2 * (2 * 132 * 2.0 ** -24 * zmag + 2.0 ** -20)[..., None]
+    tol = out_step * np.abs(out) + weight * (2.0 ** -11 + dz + 2.0 ** -11) + 2.0 ** -32 * unit + 2.0 ** -133
+    for form, s in (("dense", None), ("selected", sel)):
+        got = ref.f64(decode(b, s))
+        assert np.isfinite(got).all()
+        worst = (np.abs(got - out) / tol).max()
+        assert worst <= 1.0, f"{what}, {form}: {worst:.3f} of the tolerance"
+    no_device_error()
+
+
+@pytest.mark.parametrize("g", [1, 8, 16])
+@pytest.mark.parametrize("up", [7.5, 8.5, 9.0])
+def test_least_v_scales(g, up):
+    """Values of 2^-126 * code, which bf16 holds, next to a block of larger ones that weighs 2^-up of theirs."""
+    b = one_warp([32], 2, g, 128, seed=9)
+    b.q[:] = 0
+    b.q[..., 0] = 1.0
+    b.scale = up * math.log(2)
+    first, second = b.tables[0, :2]
+    b.kc[second, :, :, 0] = ONE
+    b.vs[first], b.vs[second] = 2.0 ** -119, 2.0 ** -126
+    b.vc[first] = 0x08  # 2^-6
+    check(b, f"2^-{up}")
+    # nothing but the least scale
+    b.vs[first] = 2.0 ** -126
+    check(b, "one scale")
