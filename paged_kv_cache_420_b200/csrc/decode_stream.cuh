@@ -87,7 +87,10 @@ __device__ __forceinline__ uint32_t tile_addr_e4m3(uint32_t tile, int r, int c) 
 // summed scores.  vs is a part of a token's weight, 2^(z - m) vs, and blocks
 // may differ in it by any power of two, while the weight is used as f16: so O
 // has references of its own, m2 ~ max(z + log2 vs), and holds
-// sum 2^(z + log2 vs - m2) code, beside m and l of the softmax.
+// sum 2^(z + log2 vs - m2) code, beside m and l of the softmax.  m2 is kept as r =
+// m2 - m, and a score used by its distance from m, which is exact near m: with
+// scores of 2^23 and more a sum z + log2 vs would lose the scale, and O a power of
+// two against l.
 //
 // Both references are raised only when a value exceeds them by kRescaleSlack
 // (weights stay below 2^8), so a stage compares its values with one threshold
@@ -101,7 +104,7 @@ struct TileState {
     uint32_t qb[NT][KS][2];  // B fragments of Q^T
     float o[NT][MT][4];      // O^T accumulators
     float m[NT][2];          // reference of the scores of heads nt*8 + 2*(lane%4) + {0,1}
-    float m2[NT][2];         // e4m3: of the columns of O^T
+    float r[NT][2];          // e4m3: of the columns of O^T, less m
     float l[NT][2];          // this thread's share of the sums
     float sc[NT][2];         // e4m3: scale * log2 e times the power of two that a head's q was divided by
 
@@ -109,7 +112,7 @@ struct TileState {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) { m[nt][c] = kNoScore; m2[nt][c] = kNoScore; l[nt][c] = 0.f; }
+            for (int c = 0; c < 2; ++c) { m[nt][c] = kNoScore; r[nt][c] = 0.f; l[nt][c] = 0.f; }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -173,18 +176,19 @@ struct TileState {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                float fo = 1.f;
-                if (mx > m[nt][c] + kRescaleSlack) {
-                    const float f = ex2(m[nt][c] - mx);
+                float fo = 1.f, d = mx - m[nt][c];
+                if (d > kRescaleSlack) {
+                    const float f = ex2(-d);
                     m[nt][c] = mx;
+                    r[nt][c] -= d;
+                    d = 0.f;
                     l[nt][c] *= f;
                     if constexpr (!KV8) fo = f;
                 }
                 if constexpr (KV8) {
-                    const float y = mx + lv;
-                    if (y > m2[nt][c] + kRescaleSlack) {
-                        fo = ex2(m2[nt][c] - y);
-                        m2[nt][c] = y;
+                    if (d + lv - r[nt][c] > kRescaleSlack) {
+                        fo = ex2(r[nt][c] - (d + lv));
+                        r[nt][c] = d + lv;
                     }
                 }
 #pragma unroll
@@ -260,8 +264,8 @@ struct TileState {
                 const float f = KV8 ? sc[nt][c] * ks : scale;
                 z[nt][c] = ok0 ? (s[nt][c] + s2[nt][c]) * f : PKV_NEG_INF;
                 z[nt][c + 2] = ok1 ? (s[nt][c + 2] + s2[nt][c + 2]) * f : PKV_NEG_INF;
-                const float top = (KV8 ? fminf(m[nt][c], m2[nt][c] - lv) : m[nt][c]) + kRescaleSlack;
-                over |= fmaxf(z[nt][c], z[nt][c + 2]) > top;
+                const float top = (KV8 ? fminf(0.f, r[nt][c] - lv) : 0.f) + kRescaleSlack;
+                over |= fmaxf(z[nt][c], z[nt][c + 2]) - m[nt][c] > top;
             }
         if (__any_sync(0xffffffffu, over)) raise(z, lv);
         uint32_t pb[NT][2], pc[KV8 ? 1 : NT][2];
@@ -270,12 +274,14 @@ struct TileState {
             float p[4];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                p[c] = ex2(z[nt][c] - m[nt][c]);
-                p[c + 2] = ex2(z[nt][c + 2] - m[nt][c]);
+                const float d0 = z[nt][c] - m[nt][c], d1 = z[nt][c + 2] - m[nt][c];
+                p[c] = ex2(d0);
+                p[c + 2] = ex2(d1);
                 l[nt][c] += p[c] + p[c + 2];
                 if constexpr (KV8) {
-                    p[c] = ex2(z[nt][c] + (lv - m2[nt][c]));
-                    p[c + 2] = ex2(z[nt][c + 2] + (lv - m2[nt][c]));
+                    const float up = lv - r[nt][c];
+                    p[c] = ex2(d0 + up);
+                    p[c + 2] = ex2(d1 + up);
                 }
             }
             // accumulator layout (token row, head pair) -> operand layout of P^T
@@ -322,14 +328,14 @@ struct TileState {
     }
 
     // l summed over its lanes, and what brings a column of O^T to reference m:
-    // f twice, each half of the exponent, since m2 - m leaves fp32's range where
+    // f twice, each half of the exponent, since r leaves fp32's range where
     // V's scales lie at its ends (2^-126 is a block's of zeros).
     __device__ __forceinline__ void finish(int nt, int c, float &lsum, float &f) {
         lsum = l[nt][c];
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-        f = KV8 ? ex2(0.5f * (m2[nt][c] - m[nt][c])) : 1.f;
+        f = KV8 ? ex2(0.5f * r[nt][c]) : 1.f;
     }
 
     // This warp's part (m, l, O) of a unit: rows of `stride` floats.

@@ -39,24 +39,39 @@ def decode(b, sel=None):
     return out
 
 
-def check(b, what, out_step=2.0 ** -8):
+def check(b, what, zmag=None):
     """Dense, and with every block selected.  |got - out| within `_block_ref.assert_attention`'s roundings, but an f16
     product is at most 2^15 where the reference of its column is 1 * 2^7, so its spacing of 2^-24 below 2^-14 is 2^-31
     of the largest product, and half of that is what a product is off by at most; and bf16's own spacing below its
-    normal range, 2^-133, in place of an absolute term."""
+    normal range, 2^-133, in place of an absolute term.  zmag: the largest sum |q k| scale, for scores without rounding."""
     n = b.tables.shape[1]
     every = np.where(np.arange(n) * b.bs < b.ctx[:, None], np.arange(n), -1)
     sel = np.ascontiguousarray(np.broadcast_to(every[:, None], (len(b.ctx), b.H, n)).astype(np.int32))
-    out, weight, zmag, unit = ref.attend(ref.f64(b.q), ref.values(b.kc, b.ks), ref.values(b.vc, b.vs), b.tables, b.ctx,
+    out, weight, most, unit = ref.attend(ref.f64(b.q), ref.values(b.kc, b.ks), ref.values(b.vc, b.vs), b.tables, b.ctx,
                                          b.scale, b.bs, v_scales=b.vs)
-    dz = 2 * (2 * 132 * 2.0 ** -24 * zmag + 2.0 ** -20)[..., None]
-    tol = out_step * np.abs(out) + weight * (2.0 ** -11 + dz + 2.0 ** -11) + 2.0 ** -32 * unit + 2.0 ** -133
+    dz = 2 * (2 * 132 * 2.0 ** -24 * (most if zmag is None else most * zmag) + 2.0 ** -20)[..., None]
+    tol = 2.0 ** -8 * np.abs(out) + weight * (2.0 ** -11 + dz + 2.0 ** -11) + 2.0 ** -32 * unit + 2.0 ** -133
     for form, s in (("dense", None), ("selected", sel)):
         got = ref.f64(decode(b, s))
         assert np.isfinite(got).all()
         worst = (np.abs(got - out) / tol).max()
         assert worst <= 1.0, f"{what}, {form}: {worst:.3f} of the tolerance"
     no_device_error()
+
+
+@pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128)])
+@pytest.mark.parametrize("power", [17, 22, 25, 40])
+def test_equal_scores_of_any_size(g, D, power):
+    """All keys alike: the row is the mean of the values, whatever the score that they share."""
+    b = one_warp([64, 33, 5], 2, g, D, seed=power)
+    b.kc[..., 0] = ONE
+    b.q[:] = 0
+    b.q[..., 0] = 1.25
+    b.scale = 2.0 ** power
+    b.vs = (2.0 ** np.random.default_rng(power).integers(-9, 9, b.vs.shape)).astype(np.float32)
+    for scale in (b.scale, -b.scale):
+        b.scale = scale
+        check(b, f"2^{power}", zmag=0.0)
 
 
 @pytest.mark.parametrize("g", [1, 8, 16])
