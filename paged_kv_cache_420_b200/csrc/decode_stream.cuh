@@ -45,6 +45,15 @@ namespace pkv {
 // -infinity weighs 0 from the first stage on (-infinity would leave NaN there).
 constexpr float kNoScore = -3.402823466e38f;
 
+// e4m3 pool: a weight times its V scale is at most 2^kRescaleSlack of its
+// reference and enters the weighted sum as f16 times 2^kWeightUp, at most 2^15.
+// f16's normal range ends at 2^-14 and its spacing below is 2^-24: a product keeps
+// 11 bits down to 2^-21 of the reference and is dropped below 2^-32 of it only, so
+// 2^20 rows that are dropped next to one that is not are 2^-12 of the sum.
+// Without the factor they were dropped below 2^-25, 131072 rows of them 2^-8.
+constexpr float kWeightUp = 7.0f;
+static_assert(kRescaleSlack + kWeightUp < 16.f, "f16 holds the largest product");
+
 // The power of two that brings a largest magnitude into [1, 2) (1/2 .. 4 at
 // the ends of the range): q is converted to f16 with it, so its elements keep
 // 11 bits down to 2^-14 of the head's largest whatever their size.  The
@@ -87,10 +96,10 @@ __device__ __forceinline__ uint32_t tile_addr_e4m3(uint32_t tile, int r, int c) 
 // summed scores.  vs is a part of a token's weight, 2^(z - m) vs, and blocks
 // may differ in it by any power of two, while the weight is used as f16: so O
 // has references of its own, m2 ~ max(z + log2 vs), and holds
-// sum 2^(z + log2 vs - m2) code, beside m and l of the softmax.  m2 is kept as r =
-// m2 - m, and a score used by its distance from m, which is exact near m: with
-// scores of 2^23 and more a sum z + log2 vs would lose the scale, and O a power of
-// two against l.
+// sum 2^(z + log2 vs - m2 + kWeightUp) code, beside m and l of the softmax.  m2 is
+// kept as r = m2 - m, and a score used by its distance from m, which is exact near
+// m: with scores of 2^23 and more a sum z + log2 vs would lose the scale, and O a
+// power of two against l.
 //
 // Both references are raised only when a value exceeds them by kRescaleSlack
 // (weights stay below 2^8), so a stage compares its values with one threshold
@@ -279,7 +288,7 @@ struct TileState {
                 p[c + 2] = ex2(d1);
                 l[nt][c] += p[c] + p[c + 2];
                 if constexpr (KV8) {
-                    const float up = lv - r[nt][c];
+                    const float up = lv - r[nt][c] + kWeightUp;
                     p[c] = ex2(d0 + up);
                     p[c + 2] = ex2(d1 + up);
                 }
@@ -328,14 +337,14 @@ struct TileState {
     }
 
     // l summed over its lanes, and what brings a column of O^T to reference m:
-    // f twice, each half of the exponent, since r leaves fp32's range where
+    // f twice, each half of the exponent, since the whole leaves fp32's range where
     // V's scales lie at its ends (2^-126 is a block's of zeros).
     __device__ __forceinline__ void finish(int nt, int c, float &lsum, float &f) {
         lsum = l[nt][c];
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
         lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-        f = KV8 ? ex2(0.5f * r[nt][c]) : 1.f;
+        f = KV8 ? ex2(0.5f * (r[nt][c] - kWeightUp)) : 1.f;
     }
 
     // This warp's part (m, l, O) of a unit: rows of `stride` floats.

@@ -59,6 +59,26 @@ def check(b, what, zmag=None):
     no_device_error()
 
 
+@pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128), (11, 64)])
+@pytest.mark.parametrize("below", [14.5, 20.4, 26.3])
+def test_weights_far_below_the_largest(g, D, below):
+    """One token outweighs the others by 2^below and has no value in half of the columns, where the row is made of the
+    others alone."""
+    b = one_warp([64, 41], 2, g, D, seed=int(below))
+    gen = torch.Generator().manual_seed(g)
+    b.q = (torch.randn(b.q.shape, generator=gen) * 0.002).to(torch.bfloat16)
+    b.q[..., 0] = 1.0
+    b.scale = below * math.log(2)
+    r = np.random.default_rng(D)
+    b.kc[..., 1:] = r.choice(np.array([0x30, 0x38, 0xB0, 0xB8], np.uint8), b.kc[..., 1:].shape)
+    b.vs = (2.0 ** r.integers(-2, 3, b.vs.shape)).astype(np.float32)
+    for s in range(2):
+        blk = b.tables[s, 0]
+        b.kc[blk, :, 5, 0] = ONE
+        b.vc[blk, :, 5, ::2] = 0
+    check(b, f"2^-{below}")
+
+
 @pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128)])
 @pytest.mark.parametrize("power", [17, 22, 25, 40])
 def test_equal_scores_of_any_size(g, D, power):
