@@ -358,11 +358,12 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  * paged_attn_decode_fp8_block: paged_attn_decode over this pool, at head
  *   dimensions 64 and 128 and every GQA group <= 16, without a partition size:
  *   the work of all sequences is divided evenly over the GPU.  Scales are finite and
- *   above zero for the blocks under a context.  The codes and q (divided by a
- *   power of two for each head) are multiplied as f16 with fp32 accumulation;
- *   a softmax weight times its block's V scale enters the weighted sum as f16,
- *   relative to the largest such product so far, whatever the scales' range: it
- *   keeps 11 bits down to 2^-21 of that, and below is rounded to 2^-31 of it.
+ *   above zero for the blocks under a context.  The codes and q (times a
+ *   power of two for each head, so that an element keeps its 8 bits down to 2^-31
+ *   of the head's largest) are multiplied as f16 with fp32 accumulation; a softmax
+ *   weight times its block's V scale enters the weighted sum as f16, relative to
+ *   the largest such product so far, whatever the scales' range: it keeps 11 bits
+ *   down to 2^-21 of that, and below is rounded to 2^-31 of it.
  *   The workspace (pkv_decode_fp8_block_workspace_bytes, 256-B aligned) is used
  *   as paged_attn_decode's.  Two kernels (attention, merge).
  */

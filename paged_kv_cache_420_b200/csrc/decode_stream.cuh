@@ -54,14 +54,14 @@ constexpr float kNoScore = -3.402823466e38f;
 constexpr float kWeightUp = 7.0f;
 static_assert(kRescaleSlack + kWeightUp < 16.f, "f16 holds the largest product");
 
-// The power of two that brings a largest magnitude into [1, 2) (1/2 .. 4 at
-// the ends of the range): q is converted to f16 with it, so its elements keep
-// 11 bits down to 2^-14 of the head's largest whatever their size.  The
-// inverse, for the scores, is exact too.
+// The power of two that brings a largest magnitude into [2^14, 2^15) (below that
+// for less than 2^-112): q is converted to f16 with it, so that an element keeps
+// its 8 bits down to 2^-31 of the head's largest whatever their size.  The inverse,
+// for the scores, is exact too.
 __device__ __forceinline__ void unit_power(float amax, float &down, float &up) {
-    const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
-    down = __uint_as_float((uint32_t)(254 - e) << 23);
-    up = __uint_as_float((uint32_t)e << 23);
+    const int e = min(max((int)(__float_as_uint(amax) >> 23), 15), 254);
+    down = __uint_as_float((uint32_t)(268 - e) << 23);
+    up = __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x; results below 2^-126 are 0

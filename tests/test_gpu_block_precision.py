@@ -79,6 +79,21 @@ def test_weights_far_below_the_largest(g, D, below):
     check(b, f"2^-{below}")
 
 
+@pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128), (11, 64)])
+@pytest.mark.parametrize("shift", [0, -100, 100])
+def test_query_with_one_large_element(g, D, shift):
+    """The scores come from the elements at 2^-22 of the largest one, which meets keys of zero."""
+    b = one_warp([64, 30], 2, g, D, seed=7)
+    gen = torch.Generator().manual_seed(g)
+    b.q = (torch.randn(b.q.shape, generator=gen) * 2.0 ** (shift - 22)).to(torch.bfloat16)
+    b.q[..., 0] = 2.0 ** shift
+    b.scale = 2.0 ** -shift
+    r = np.random.default_rng(D)
+    b.kc[..., 1:] = r.integers(0, 0x60, b.kc[..., 1:].shape) | r.choice(np.array([0, 0x80]), b.kc[..., 1:].shape)
+    b.ks[:] = 2.0 ** 16
+    check(b, f"2^{shift}")
+
+
 @pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128)])
 @pytest.mark.parametrize("power", [17, 22, 25, 40])
 def test_equal_scores_of_any_size(g, D, power):
