@@ -436,8 +436,9 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *               whose scores are all -infinity.
  *     k_scales, v_scales  NULL for a bf16 pool; the block scales of an e4m3 pool
  *   Both pools at head dimensions 64 and 128 and every GQA group <= 16, with
- *   fp32 sums; the weights enter the weighted sum rounded to 17 bits over a
- *   bf16 pool, and as in paged_attn_decode_fp8_block over an e4m3 pool.  The
+ *   fp32 sums; the weights enter the weighted sum rounded to 16 bits over a
+ *   bf16 pool (where an infinite V of a weight above 2^-100 gives an infinite
+ *   sum), and as in paged_attn_decode_fp8_block over an e4m3 pool.  The
  *   workspace (pkv_decode_sparse_workspace_bytes, 256-B aligned) is used as
  *   paged_attn_decode's.  Two kernels (attention, merge).
  */

@@ -88,8 +88,10 @@ __device__ __forceinline__ uint32_t tile_addr_e4m3(uint32_t tile, int r, int c) 
 // tensor cores: a warp issues one every four cycles, so what is done for each
 // stage beside the products and conversions is kept small.
 //
-// bf16 pool: the weights enter the second product as a sum of two bf16 (17
-// bits): twice the products, which are free.
+// bf16 pool: the weights enter the second product as a sum of two bf16 (16
+// bits): twice the products, which are free.  Both are above zero, the first cut
+// off instead of rounded and the last bit of the weight set, so that an infinite
+// V gives an infinite sum: beside a negative or a zero second one it gave NaN.
 //
 // e4m3 pool, scales ks and vs of the stage's block: the codes are exact as
 // f16, and a stage's tokens are taken in perm16 order.  ks multiplies the
@@ -298,7 +300,10 @@ struct TileState {
                 pb[nt][0] = movmatrix_trans(f16x2_from_f32(p[0], p[1]));
                 pb[nt][1] = movmatrix_trans(f16x2_from_f32(p[2], p[3]));
             } else {
-                const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[c] = __uint_as_float(__float_as_uint(p[c]) | 1u);
+                const uint32_t h0 = __byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632);
+                const uint32_t h1 = __byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632);
                 pb[nt][0] = movmatrix_trans(h0);
                 pb[nt][1] = movmatrix_trans(h1);
                 pc[nt][0] = movmatrix_trans(pack_bf16x2(p[0] - bf16lo_to_f32(h0), p[1] - bf16hi_to_f32(h0)));

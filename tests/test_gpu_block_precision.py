@@ -125,3 +125,32 @@ def test_least_v_scales(g, up):
     # nothing but the least scale
     b.vs[first] = 2.0 ** -126
     check(b, "one scale")
+
+
+@pytest.mark.parametrize("g,D", [(1, 128), (4, 64), (16, 128), (8, 128)])
+@pytest.mark.parametrize("blocks", [2, 40])
+def test_infinite_values_of_a_bf16_pool(g, D, blocks):
+    """A value of infinity gives an infinite sum in its column alone, and NaN only where both signs meet."""
+    b = ref.Batch([16 * blocks - 3], [1], 2, D, 16, seed=blocks, g=g)
+    b.ks[:] = 2.0 ** -9  # scores of some units: no weight is below 2^-100
+    k, v = b.bf16_pool()
+    for h in range(2):
+        for i, col in enumerate(range(0, D, 5)):
+            v[b.tables[0, i % blocks], h, i % 13, col] = float("inf") if i % 2 else float("-inf")
+        v[b.tables[0, 0], h, 3, 7], v[b.tables[0, 1], h, 2, 7] = float("inf"), float("-inf")
+        # the largest score: its weight is 1 exactly
+        v[b.tables[0, 0], h, 0, 11] = float("inf")
+        k[b.tables[0, 0], h, 0] = 6 * b.q[0, h * g] / b.q[0, h * g].float().norm()
+    sel = np.ascontiguousarray(np.broadcast_to(np.arange(blocks, dtype=np.int32), (1, 2, blocks)))
+    out = torch.empty((1, 2 * g, D), dtype=torch.bfloat16, device="cuda")
+    pkv.paged_attn_decode_sparse(cuda(b.q), cuda(k), cuda(v), cuda(b.tables), cuda(b.ctx), cuda(sel), b.scale, 2, out)
+    with np.errstate(invalid="ignore"):
+        want = ref.attend(ref.f64(b.q), ref.f64(k), ref.f64(v), b.tables, b.ctx, b.scale, 16, sel)
+    got, finite = ref.f64(out), np.isfinite(want[0])
+    assert np.array_equal(got[~finite], want[0][~finite], equal_nan=True)
+    assert np.isnan(got[..., 7]).all() and (got[..., 11] == np.inf).all()
+    dz = 2 * (2 * 132 * 2.0 ** -24 * want[2] + 2.0 ** -20)[..., None]
+    with np.errstate(invalid="ignore"):
+        tol = 2.0 ** -8 * np.abs(want[0]) + want[1] * (2.0 ** -16 + dz + 2.0 ** -11)
+    assert (np.abs(got[finite] - want[0][finite]) <= tol[finite]).all()
+    no_device_error()
