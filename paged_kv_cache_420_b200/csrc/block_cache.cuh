@@ -80,7 +80,9 @@ constexpr int kTouchTeams = 4;  // teams of one warp in a CTA
 //   all others: code' = e4m3(e4m3(code) s / s'), only when s' > s > 0
 // A power of two makes both products exact in fp32 (so each element is rounded
 // once, ties to even, saturating; fp32 underflow rounds to a zero code), and
-// growing a scale exact for every code that stays a normal e4m3 number.
+// growing a scale exact for every code that stays a normal e4m3 number.  Another
+// old scale that is large enough stays, and x is divided by it: the product with
+// its reciprocal would be rounded twice, and miss ties (175 / 7 = 25).
 struct WriteBlockParams {
     TouchParams t;
     const uint4 *k;  // [T][H][D] bf16 as 16-byte vectors
@@ -135,6 +137,19 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     const float2 a = f32x2_from_f16x2(f16x2_from_e4m3x2(w & 0xffffu));
     const float2 b = f32x2_from_f16x2(f16x2_from_e4m3x2(w >> 16));
     return e4m3x2_from_f32(a.x * ratio, a.y * ratio) | (e4m3x2_from_f32(b.x * ratio, b.y * ratio) << 16);
+}
+
+// The codes of n rows of x (`stride` pairs apart) divided by s, two at a time from
+// pair `at` in steps of `step`: rare, and a function of its own so that the
+// quotient costs the kernel no registers.
+template <int D>
+__device__ __noinline__ void write_divided(const uint32_t *x, size_t stride, float s, int n, int at, int step,
+                                           uint16_t *code) {
+#pragma unroll 1
+    for (; at < n * (D / 2); at += step) {
+        const uint32_t w = __ldg(x + (size_t)(at / (D / 2)) * stride + at % (D / 2));
+        code[at] = (uint16_t)e4m3x2_from_f32(__fdiv_rn(bf16lo_to_f32(w), s), __fdiv_rn(bf16hi_to_f32(w), s));
+    }
 }
 
 // PASSES: rows of a group / rows of a pass (fewer for short appends, whose
@@ -210,7 +225,10 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) write_fp8_block_kernel(co
     }
     const float grown = fmaxf(s_old, pow2_scale(amax));
     const float inv = __frcp_rn(grown);  // exact for a power of two
-    for (int grp = wt; grp * GROUP < fresh; grp += p.W) {
+    if ((__float_as_uint(grown) & 0x7fffffu) != 0) {  // no power of two
+        write_divided<D>(reinterpret_cast<const uint32_t *>(x), stride * 4, grown, fresh, wt * 32 + lane, p.W * 32,
+                         reinterpret_cast<uint16_t *>(cache + (size_t)t.old * VPR));
+    } else for (int grp = wt; grp * GROUP < fresh; grp += p.W) {
         if (grp != loaded) load(grp);
         loaded = grp;
 #pragma unroll

@@ -154,3 +154,31 @@ def test_infinite_values_of_a_bf16_pool(g, D, blocks):
         tol = 2.0 ** -8 * np.abs(want[0]) + want[1] * (2.0 ** -16 + dz + 2.0 ** -11)
     assert (np.abs(got[finite] - want[0][finite]) <= tol[finite]).all()
     no_device_error()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,bs", [(1, 16), (7, 16), (1, 48), (40, 64)])
+def test_write_under_an_old_scale_that_is_no_power_of_two(D, new, bs):
+    """The quotient x / scale rounded to fp32 once, then to e4m3: quotients that are ties, and scales whose reciprocal
+    is below fp32's normal range."""
+    r = np.random.default_rng(D + new)
+    scales = [7.0, 3.0, 49.0, 2.0 ** 126 * 1.5, 3e38, 1e-30] + [float(x) for x in np.exp(r.uniform(-60, 60, 26))]
+    n = len(scales)
+    b = ref.Batch([9 + new] * n, [new] * n, 2, D, bs, seed=1)
+    b.ks[b.tables[:, 0]] = b.vs[b.tables[:, 0]] = np.asarray(scales, np.float32)[:, None]
+    t = np.repeat(np.arange(n), new)
+    s = np.asarray(scales, np.float64)[t, None, None]
+    # values whose quotients are ties or near them, and any; below 224 scales, so that none of them grows
+    odd = r.integers(16, 32, (len(t), 2, D)) * 2.0 ** r.integers(-6, 3, (len(t), 2, D))
+    k = torch.from_numpy(np.clip(odd * s, -3e38, 3e38)).to(torch.bfloat16)
+    v = torch.from_numpy(np.clip(s * 60 * r.standard_normal((len(t), 2, D)).clip(-3.5, 3.5), -3e38, 3e38)).to(torch.bfloat16)
+    kc, vc, ks, vs = (cuda(x.copy()) for x in (b.kc, b.vc, b.ks, b.vs))
+    pkv.pkv_write_fp8_block(cuda(k), cuda(v), cuda(b.tables), cuda(b.ctx), cuda(b.start), ks, vs, kc, vc, new)
+    assert np.array_equal(ks.cpu().numpy(), b.ks) and np.array_equal(vs.cpu().numpy(), b.vs)
+    for got, was, x in ((kc, b.kc, k), (vc, b.vc, v)):
+        want = was.copy()
+        quotient = x.float().numpy() / np.asarray(scales, np.float32)[t, None, None]
+        for i in range(len(t)):
+            want[b.tables[t[i], 0], :, 9 + i % new] = oracle.e4m3_encode(quotient[i].astype(np.float64))
+        assert ref.same_codes(got.cpu().numpy(), want)
+    no_device_error()
