@@ -442,8 +442,6 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     _check(st, "paged_attn_decode_fp8")
 
 
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 _WRITE_TYPES = (_BF16, _BF16, _I32, _I32, _I32, _F32, _F32, _U8, _U8)
 _DECODE_TYPES = (_BF16, _BF16, _U8, _U8, _F32, _F32, _I32, _I32)
@@ -472,11 +470,12 @@ def _pool_of(num_blocks, num_kv_heads, block_size, head_dim, kv_dtype):
 
 def _launch(what: str, index: int, stream, f, *args) -> None:
     """Calls f(*args, stream) with GPU `index` current; stream None: that GPU's current stream."""
+    # torch.cuda's own forms of both getters take 5 us more a call; a torch without CUDA has neither
     if stream is None:
-        raw = _current_raw_stream(index)
+        raw = torch._C._cuda_getCurrentRawStream(index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    previous = _current_device()
+    previous = torch._C._cuda_getDevice()
     if index == previous:
         status = f(*args, raw)
     else:
