@@ -129,13 +129,18 @@ pkv_status pkv_copy_blocks(const int32_t *src_dst_pairs, int32_t num_pairs, void
  *   block_ids        HOST int32 [n], ids in [0, num_blocks) (else PKV_ERANGE)
  *   host_k, host_v   pinned host memory the device can address (cudaHostAlloc /
  *                    cudaMallocHost / a pinned torch tensor), 16-B aligned, each
- *                    n * num_kv_heads * block_size * head_dim bf16, packed in
- *                    list order: entry i is [num_kv_heads][block_size][head_dim].
+ *                    n * num_kv_heads * block_size * head_dim elements of the pool
+ *                    (bf16, or one byte), packed in list order: entry i is
+ *                    [num_kv_heads][block_size][head_dim].
  *                    Pageable or device memory gives PKV_EINVAL.
  * swap_out: host_k[i] / host_v[i] become bit-exact copies of block ids[i] of
  *           k_cache / v_cache (the pool is only read; ids may repeat).
  * swap_in:  block ids[i] of both caches becomes host_k[i] / host_v[i]; ids must
  *           be distinct (PKV_EALIAS).
+ * Only K and V move.  What else is kept for a block by its id -- the block scales
+ * of pkv_write_fp8_block, the bounds of pkv_key_bounds -- is the caller's to save
+ * beside it and to put back under the new id; codes under another block's scales
+ * are other values, and nothing reports that.
  * Asynchronous on `stream`: the host buffers must stay alive and untouched
  * until the stream reaches the call.  n == 0 is a no-op; nothing is enqueued
  * when validation fails.
@@ -321,7 +326,9 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  * block b and kv head h is e4m3(c) * scales[b][h].  The pages name FP8 mixed
  * precision (ai-stack.site "Nano-vLLM 原理", case study) and have no
  * counterpart of the scales.  A block's scales travel with its codes: copy
- * both on copy-on-write (pkv_copy_blocks / _dev and pkv_copy_scales / _dev).
+ * both on copy-on-write (pkv_copy_blocks / _dev and pkv_copy_scales / _dev), and
+ * on a swap save row ids[i] of both arrays beside host_k[i] / host_v[i] and write
+ * it back as the row of the block that pkv_swap_in fills.
  *
  * pkv_write_fp8_block: appends tokens and quantises them.  Sequence s gets the
  *   rows query_start[s] .. query_start[s+1] - 1 of k and v (bf16 [num_tokens]
@@ -397,7 +404,11 @@ size_t pkv_decode_fp8_block_workspace_bytes(int32_t num_seqs, int32_t num_q_head
  *   write).  bounds is bf16 [num_blocks][num_kv_heads][2][head_dim] (least
  *   first), 16-B aligned; other blocks' bounds stay as they were.  k_scales is
  *   NULL for a bf16 pool and the block scales of an e4m3 pool (whose values
- *   are rounded to bf16).  A column with a NaN key has NaN bounds.
+ *   are rounded to bf16).  A column with a NaN key has NaN bounds.  A block that
+ *   is filled in another way (pkv_copy_blocks without an append, pkv_swap_in)
+ *   needs its row of bounds copied, or a call over its sequence whole: every block
+ *   of a sequence counts as touched when query_start gives it as many tokens as
+ *   context_lens.
  */
 pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int32_t *block_tables,
                           int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,

@@ -202,7 +202,9 @@ def _block_ids(block_ids) -> np.ndarray:
 def pkv_swap_out(k_cache: torch.Tensor, v_cache: torch.Tensor, block_ids, host_k: torch.Tensor,
                  host_v: torch.Tensor, stream=None) -> None:
     """host_k[i] / host_v[i] := block block_ids[i] of k_cache / v_cache (pinned
-    host tensors of at least len(block_ids) blocks); asynchronous on the stream."""
+    host tensors of at least len(block_ids) blocks); asynchronous on the stream.
+    Only K and V move: a block's scales (pkv_write_fp8_block) and bounds (pkv_key_bounds) are rows
+    block_ids[i] of arrays of the caller's, to be saved beside it."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need_cache(t, n)
     ids = _block_ids(block_ids)
@@ -215,7 +217,8 @@ def pkv_swap_out(k_cache: torch.Tensor, v_cache: torch.Tensor, block_ids, host_k
 
 def pkv_swap_in(host_k: torch.Tensor, host_v: torch.Tensor, block_ids, k_cache: torch.Tensor,
                 v_cache: torch.Tensor, stream=None) -> None:
-    """Block block_ids[i] of k_cache / v_cache := host_k[i] / host_v[i] (ids distinct)."""
+    """Block block_ids[i] of k_cache / v_cache := host_k[i] / host_v[i] (ids distinct).
+    Rows block_ids[i] of block scales and bounds are to be put back as pkv_swap_out's caller saved them."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need_cache(t, n)
     ids = _block_ids(block_ids)
