@@ -403,8 +403,8 @@ size_t pkv_decode_fp8_block_workspace_bytes(int32_t num_seqs, int32_t num_q_head
  *   append touches (arguments as in pkv_write_fp8_block; run it after the
  *   write).  bounds is bf16 [num_blocks][num_kv_heads][2][head_dim] (least
  *   first), 16-B aligned; other blocks' bounds stay as they were.  k_scales is
- *   NULL for a bf16 pool and the block scales of an e4m3 pool (whose values
- *   are rounded to bf16).  A column with a NaN key has NaN bounds.  A block that
+ *   NULL for a bf16 pool and the block scales of an e4m3 pool (where a least
+ *   key that is no bf16 is rounded down and a largest one up).  A column with a NaN key has NaN bounds.  A block that
  *   is filled in another way (pkv_copy_blocks without an append, pkv_swap_in)
  *   needs its row of bounds copied, or a call over its sequence whole: every block
  *   of a sequence counts as touched when query_start gives it as many tokens as

@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(256) copy_scales_dev_kernel(float *k_scales, f
 // of them is NaN; [NB][H][2][D] bf16, lo first.  Every held row is read, not
 // only the new ones: a block that was copied or whose scale has grown needs no
 // other care.  Over an 8-bit pool the least and largest CODE are found and
-// scaled once (the scale is positive, and rounding to bf16 keeps the order).
+// scaled once (the scale is positive).  The product is exact in bf16 where the scale
+// is a power of two and nothing leaves bf16's normal range; otherwise the least is
+// rounded down and the largest up, so that every key lies between them.
 // Sign-magnitude numbers order alike whatever their fields, so a code is
 // compared as the upper byte of a bf16: what lies in the lower one decides
 // between equal codes only, and 0x7f and 0xff, the NaN codes, stay at an end or
@@ -312,6 +314,13 @@ __device__ __forceinline__ void min_max_bf16x2(uint32_t &lo, uint32_t &hi, uint3
     asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(l));
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(h));
 }
+
+// code * s as the next bf16 below it, or above.
+__device__ __forceinline__ float scaled_down(float code, float s) {
+    const uint32_t u = __float_as_uint(__fmul_rd(code, s));
+    return __uint_as_float(((u & 0xffffu) != 0 && (u >> 31) ? u + 0x10000u : u) & 0xffff0000u);
+}
+__device__ __forceinline__ float scaled_up(float code, float s) { return -scaled_down(-code, s); }
 
 // The upper bytes of `even` and `odd`, codes of columns 0, 2 and 1, 3, as values.
 __device__ __forceinline__ void values_of_codes(uint32_t even, uint32_t odd, float (&x)[4]) {
@@ -384,6 +393,9 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
         }
     }
     if constexpr (KV8) {
+        // a code is 2^-9 at least and 448 at most, bf16 2^-133 and below 2^128
+        const uint32_t sb = __float_as_uint(ks), se = sb >> 23;
+        const bool exact = (sb & 0x7fffffu) == 0 && se >= 127 - 124 && se <= 127 + 119;
 #pragma unroll
         for (int v = 0; v < 4; v += 2) {  // word v / 2 of the row's codes
             float l[4], g[4];
@@ -392,8 +404,8 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool nan = l[e] != l[e] || g[e] != g[e];
-                l[e] = nan ? __int_as_float(0x7fffffff) : l[e] * ks;
-                g[e] = nan ? __int_as_float(0x7fffffff) : g[e] * ks;
+                l[e] = nan ? __int_as_float(0x7fffffff) : exact ? l[e] * ks : scaled_down(l[e], ks);
+                g[e] = nan ? __int_as_float(0x7fffffff) : exact ? g[e] * ks : scaled_up(g[e], ks);
             }
             lo[v] = pack_bf16x2(l[0], l[1]);
             lo[v + 1] = pack_bf16x2(l[2], l[3]);

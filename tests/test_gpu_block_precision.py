@@ -182,3 +182,32 @@ def test_write_under_an_old_scale_that_is_no_power_of_two(D, new, bs):
             want[b.tables[t[i], 0], :, 9 + i % new] = oracle.e4m3_encode(quotient[i].astype(np.float64))
         assert ref.same_codes(got.cpu().numpy(), want)
     no_device_error()
+
+
+def outward(x, up):
+    """fp64 values as the nearest bf16 that is not below them (up), or not above."""
+    sign = 1.0 if up else -1.0
+    y = torch.from_numpy(x * sign).to(torch.bfloat16)
+    y = torch.where(y.double() < torch.from_numpy(x * sign), torch.nextafter(y, torch.full_like(y, float("inf"))), y)
+    return y.double().numpy() * sign
+
+
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 48)])
+def test_bounds_hold_the_keys_under_any_scale(D, bs):
+    """Scales that are no powers of two, and powers of two whose products leave bf16's normal range: the least key is
+    rounded down, the largest up."""
+    scales = [0.1, 7.0, 1e-38, 3e35, 2.0 ** -126, 2.0 ** -125, 2.0 ** -124, 2.0 ** 119, 2.0 ** 120, 3e38]
+    r = np.random.default_rng(D)
+    scales += [float(x) for x in np.exp(r.uniform(-80, 80, 20))]
+    b = ref.Batch([bs] * len(scales), [bs] * len(scales), 2, D, bs, seed=3)
+    b.ks[b.tables[:, 0]] = np.asarray(scales, np.float32)[:, None]
+    b.kc[b.tables[:5, 0], :, :, :5] = np.array([0x00, 0x01, 0x81, 0x80, 0x7E], np.uint8)  # whole columns
+    got = torch.zeros((b.NB, 2, 2, D), dtype=torch.bfloat16, device="cuda")
+    pkv.pkv_key_bounds(cuda(b.kc), cuda(b.tables), cuda(b.ctx), cuda(b.start), got, bs, k_scales=cuda(b.ks))
+    at = b.tables[:, 0]
+    keys, got = ref.values(b.kc, b.ks)[at], ref.f64(got)[at]
+    assert (got[:, :, 0] <= keys.min(2)).all() and (got[:, :, 1] >= keys.max(2)).all()
+    big = torch.finfo(torch.bfloat16).max
+    assert np.array_equal(got[:, :, 0], np.minimum(outward(keys.min(2), False), big))
+    assert np.array_equal(got[:, :, 1], np.maximum(outward(keys.max(2), True), -big))
+    no_device_error()
