@@ -355,7 +355,12 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  *   sequence with more new tokens than max_new_tokens or its context, with
  *   rows outside [0, num_tokens), or longer than its table sets
  *   PKV_DEVERR_CONTEXT and is left out; a block id outside the pool sets
- *   PKV_DEVERR_BLOCK and the block is left out.  One kernel, no workspace.
+ *   PKV_DEVERR_BLOCK and the block is left out.  With num_seqs, num_tokens or
+ *   max_new_tokens 0 nothing is done or looked at.  One kernel, no workspace; its
+ *   grid has a place for num_seqs * num_kv_heads * 2 times the blocks that
+ *   max_new_tokens can touch (above 2^31 - 1: PKV_EUNSUPPORTED), so a tight bound
+ *   is faster, and a chunk of a prompt is better appended in a call of its own
+ *   than among sequences with one token each.
  *
  * pkv_copy_scales / pkv_copy_scales_dev: row src -> row dst of both scale
  *   arrays for every pair, with the rules of pkv_copy_blocks (host pairs) and
@@ -372,7 +377,9 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  *   the largest such product so far, whatever the scales' range: it keeps 11 bits
  *   down to 2^-21 of that, and below is rounded to 2^-31 of it.
  *   The workspace (pkv_decode_fp8_block_workspace_bytes, 256-B aligned) is used
- *   as paged_attn_decode's.  Two kernels (attention, merge).
+ *   as paged_attn_decode's.  Two kernels (attention, merge), or one where
+ *   max_context_len is at most 64, or 256 with 2368 (sequence, kv head) pairs and
+ *   more.  paged_attn_prefill reads bf16 pools only (PKV_EINVAL).
  */
 pkv_status pkv_write_fp8_block(const void *k, const void *v, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
@@ -408,7 +415,8 @@ size_t pkv_decode_fp8_block_workspace_bytes(int32_t num_seqs, int32_t num_q_head
  *   is filled in another way (pkv_copy_blocks without an append, pkv_swap_in)
  *   needs its row of bounds copied, or a call over its sequence whole: every block
  *   of a sequence counts as touched when query_start gives it as many tokens as
- *   context_lens.
+ *   context_lens.  What is said there of zero sizes, of the grid (without the
+ *   factor 2) and of a tight max_new_tokens holds here.
  */
 pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int32_t *block_tables,
                           int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,
@@ -428,8 +436,10 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *               either kv_dtype)
  *     selected  int32 [num_seqs][num_kv_heads][num_selected], num_selected >= 2:
  *               ascending logical blocks, then -1
- *     max_context_len  host upper bound of context_lens (sizes the workspace;
- *               above 800000 blocks: PKV_EUNSUPPORTED)
+ *     max_context_len  host upper bound of context_lens (above 800000 blocks:
+ *               PKV_EUNSUPPORTED).  It sizes the workspace, 16 bytes for each
+ *               sequence, kv head and block of the bound, and the selecting
+ *               CTAs: the closer, the faster (up to 1.8 times)
  *     workspace  at least pkv_select_workspace_bytes(...), 256-B aligned, as in
  *               paged_attn_decode
  *   A context length < 0 or above the table / max_context_len sets
