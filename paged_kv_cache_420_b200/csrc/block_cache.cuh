@@ -396,22 +396,27 @@ __global__ void __launch_bounds__(kTouchMaxWarps * 32) key_bounds_kernel(const K
         // a code is 2^-9 at least and 448 at most, bf16 2^-133 and below 2^128
         const uint32_t sb = __float_as_uint(ks), se = sb >> 23;
         const bool exact = (sb & 0x7fffffu) == 0 && se >= 127 - 124 && se <= 127 + 119;
+        auto scale = [&](auto &&down, auto &&up) {
 #pragma unroll
-        for (int v = 0; v < 4; v += 2) {  // word v / 2 of the row's codes
-            float l[4], g[4];
-            values_of_codes(lo[v], lo[v + 1], l);
-            values_of_codes(hi[v], hi[v + 1], g);
+            for (int v = 0; v < 4; v += 2) {  // word v / 2 of the row's codes
+                float l[4], g[4];
+                values_of_codes(lo[v], lo[v + 1], l);
+                values_of_codes(hi[v], hi[v + 1], g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool nan = l[e] != l[e] || g[e] != g[e];
-                l[e] = nan ? __int_as_float(0x7fffffff) : exact ? l[e] * ks : scaled_down(l[e], ks);
-                g[e] = nan ? __int_as_float(0x7fffffff) : exact ? g[e] * ks : scaled_up(g[e], ks);
+                for (int e = 0; e < 4; ++e) {
+                    const bool nan = l[e] != l[e] || g[e] != g[e];
+                    l[e] = nan ? __int_as_float(0x7fffffff) : down(l[e], ks);
+                    g[e] = nan ? __int_as_float(0x7fffffff) : up(g[e], ks);
+                }
+                lo[v] = pack_bf16x2(l[0], l[1]);
+                lo[v + 1] = pack_bf16x2(l[2], l[3]);
+                hi[v] = pack_bf16x2(g[0], g[1]);
+                hi[v + 1] = pack_bf16x2(g[2], g[3]);
             }
-            lo[v] = pack_bf16x2(l[0], l[1]);
-            lo[v + 1] = pack_bf16x2(l[2], l[3]);
-            hi[v] = pack_bf16x2(g[0], g[1]);
-            hi[v + 1] = pack_bf16x2(g[2], g[3]);
-        }
+        };
+        auto product = [](float x, float y) { return x * y; };
+        if (exact) scale(product, product);
+        else scale(scaled_down, scaled_up);
     }
     if (lane < VPR) {
         uint4 *out = p.bounds + head * 2 * VPR;
