@@ -502,7 +502,9 @@ def _scratch(workspace: Optional[torch.Tensor], nbytes: int, index: int, stream)
         ws = torch.empty(nbytes, dtype=_U8, device=index)
     else:  # `stream`'s memory: what the current stream has let go of may still be in use there
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+            handle = int(getattr(stream, "cuda_stream", stream))
+            # (an ExternalStream of handle 0 is not the default stream, but one of torch's pool)
+            stream = torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
         with torch.cuda.stream(stream):
             ws = torch.empty(nbytes, dtype=_U8, device=index)
     return ws.data_ptr(), nbytes, ws
