@@ -435,8 +435,8 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     if out.shape != q.shape or v_cache.shape != k_cache.shape:
         raise ValueError("out must match q and v_cache must match k_cache")
     if workspace is None:
-        workspace = torch.empty(decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens),
-                                dtype=torch.uint8, device=q.device)
+        nbytes = decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens)
+        workspace = _scratch(None, nbytes, q.get_device(), stream)[2]
     st = load_library().paged_attn_decode_fp8(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
         block_tables.shape[1], _ptr(context_lens), B, Hq, float(scale), int(num_kv_heads), _ptr(out),
@@ -744,7 +744,7 @@ def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
     if workspace is None:
         nbytes = decode_workspace_bytes(B, Hq, num_kv_heads, D, max_context_len, partition_tokens)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(None, nbytes, q.get_device(), stream)[2]
     st = load_library().paged_attn_decode(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
         B, Hq, float(scale), int(num_kv_heads), _ptr(out), _pool(k_cache), int(max_context_len),
@@ -834,8 +834,8 @@ def paged_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if out.shape != q.shape or query_start.shape != (B + 1,) or block_tables.shape[0] != B:
         raise ValueError("shape mismatch among q/out, query_start [B+1], block_tables [B, MBS]")
     if workspace is None:
-        workspace = torch.empty(prefill_workspace_bytes(B, Hq, num_kv_heads, max_query_len), dtype=torch.uint8,
-                                device=q.device)
+        nbytes = prefill_workspace_bytes(B, Hq, num_kv_heads, max_query_len)
+        workspace = _scratch(None, nbytes, q.get_device(), stream)[2]
     lib = load_library()
     f = lib.paged_attn_prefill
     if f.argtypes is None:

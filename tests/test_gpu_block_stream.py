@@ -36,3 +36,30 @@ def test_a_call_on_the_default_streams_handle():
                       v_scales=b.vs)
     ref.assert_attention(outs[0], want, 2.0 ** -11)
     no_device_error()
+
+
+@pytest.mark.parametrize("call", ["decode", "decode_fp8", "prefill"])
+def test_every_attention_call_takes_its_workspace_from_its_stream(call, monkeypatch):
+    taken, scratch, stream = [], pkv._scratch, torch.cuda.Stream()
+
+    def spy(workspace, nbytes, index, on):
+        taken.append(on)
+        return scratch(workspace, nbytes, index, on)
+
+    monkeypatch.setattr(pkv, "_scratch", spy)
+    b = ref.Batch([64], [1], 2, 128, 16, seed=52, g=2)
+    q, tables, ctx = b.q.cuda(), torch.from_numpy(b.tables).cuda(), torch.from_numpy(b.ctx).cuda()
+    k, v = (x.cuda() for x in b.bf16_pool())
+    codes, scale = torch.from_numpy(b.kc).cuda(), torch.ones(2, device="cuda")
+    start, out = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    torch.cuda.synchronize()
+    for on in (None, stream):
+        if call == "decode":
+            pkv.paged_attn_decode(q, k, v, tables, ctx, b.scale, 2, out, 64, stream=on)
+        elif call == "decode_fp8":
+            pkv.paged_attn_decode_fp8(q, codes, codes, scale, scale, tables, ctx, b.scale, 2, out, 64, stream=on)
+        else:
+            pkv.paged_attn_prefill(q, k, v, tables, ctx, start, b.scale, 2, out, 1, 64, stream=on)
+        torch.cuda.synchronize()
+    assert taken == [None, stream]
+    no_device_error()
