@@ -370,7 +370,8 @@ pkv_status paged_attn_decode_fp8(const void *q, const void *k_cache, const void 
  * paged_attn_decode_fp8_block: paged_attn_decode over this pool, at head
  *   dimensions 64 and 128 and every GQA group <= 16, without a partition size:
  *   the work of all sequences is divided evenly over the GPU.  Scales are finite and
- *   above zero for the blocks under a context.  The codes and q (times a
+ *   above zero for the blocks under a context, and out overlaps no input (PKV_EALIAS
+ *   where it is q).  The codes and q (times a
  *   power of two for each head, so that an element keeps its 8 bits down to 2^-31
  *   of the head's largest) are multiplied as f16 with fp32 accumulation; a softmax
  *   weight times its block's V scale enters the weighted sum as f16, relative to
@@ -456,6 +457,7 @@ pkv_status pkv_key_bounds(const void *k_cache, const float *k_scales, const int3
  *               (or an empty context) gives a zero output row, and so do keys
  *               whose scores are all -infinity.
  *     k_scales, v_scales  NULL for a bf16 pool; the block scales of an e4m3 pool
+ *     out       overlaps no input (PKV_EALIAS where it is q)
  *   Both pools at head dimensions 64 and 128 and every GQA group <= 16, with
  *   fp32 sums; the weights enter the weighted sum rounded to 16 bits over a
  *   bf16 pool (where an infinite V of a weight above 2^-100 gives an infinite

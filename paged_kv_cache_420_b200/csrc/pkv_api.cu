@@ -914,6 +914,7 @@ pkv_status paged_attn_decode_fp8_block(const void *q, const void *k_cache, const
     const long long stages = ((long long)max_context_len + pkv::kStageTok - 1) / pkv::kStageTok;
     if (!stream_layout(num_seqs, num_q_heads, num_kv_heads, pool.head_dim, stages, &wl) || workspace_bytes < wl.total)
         return PKV_EINVAL;
+    if (out == q) return PKV_EALIAS;  // a unit's warps read q while another one writes its row
     pkv::StreamParams p;
     std::memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1125,6 +1126,7 @@ pkv_status paged_attn_decode_sparse(const void *q, const void *k_cache, const vo
                        (long long)num_selected * (pool.block_size / pkv::kStageTok), &wl) ||
         workspace_bytes < wl.total)
         return PKV_EINVAL;
+    if (out == q) return PKV_EALIAS;
     pkv::StreamParams p;
     std::memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16 *>(q);
