@@ -122,9 +122,10 @@ __device__ __forceinline__ uint32_t tile_addr_e4m3(uint32_t tile, int r, int c) 
 // of the unused columns are free, and the CUDA-core form takes twice the
 // instructions):
 //   S^T[16 tokens][8 heads] = K Q^T,  O^T[D][8 heads] += V^T P^T
-// in the fragment layouts of MmaState.  Its instructions bound it, not the
-// tensor cores: a warp issues one every four cycles, so what is done for each
-// stage beside the products and conversions is kept small.
+// in the fragment layouts of MmaState.  Beside HBM its instructions bound it, not
+// the tensor cores (issue 50%, tensor pipe 19% on long lines; a warp can issue one
+// in four cycles at best), so what is done for each stage beside the products and
+// conversions is kept small.
 //
 // bf16 pool: the weights enter the second product as a sum of two bf16 (16
 // bits): twice the products, which are free.  Both are above zero, the first cut
