@@ -44,10 +44,10 @@ __device__ __forceinline__ bool touched_block(const TouchParams &p, int s, int i
         return false;
     }
     const int p0 = c - (int)n;  // the first new token's position
-    const int j = p0 / p.bs + i;
-    if (j >= p.MBS) return false;
-    const int j0 = j * p.bs;
-    if (j0 >= c) return false;
+    const int first = p0 / p.bs;
+    // behind the context (told before a position is formed, which can pass 2^31 there)
+    if ((uint32_t)i * (uint32_t)p.bs >= (uint32_t)(p0 - first * p.bs) + (uint32_t)n) return false;
+    const int j = first + i, j0 = j * p.bs;
     const int blk = __ldg(p.tables + (size_t)s * p.MBS + j);
     if (blk < 0 || blk >= p.NB) {
         if (report) raise_error(PKV_DEVERR_BLOCK);
